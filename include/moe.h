@@ -419,6 +419,146 @@ MOE_API moe_status moe_route_noalloc(const void* x, const void* router_w, const 
                                      int32_t hidden, int32_t n_routed, int32_t top_k, float route_scale,
                                      int32_t* topk_idx, float* topk_w, moe_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Routing from given logits, and the layer with a given routing
+ * ---------------------------------------------------------------------- */
+
+typedef enum { MOE_VAL_BF16 = 0, MOE_VAL_FP16 = 1, MOE_VAL_FP32 = 2 } moe_value_dtype;
+
+typedef enum {
+  MOE_SCORE_SOFTMAX = 0,     /* over all experts */
+  MOE_SCORE_SIGMOID = 1,
+  MOE_SCORE_SQRTSOFTPLUS = 2 /* the layer's own: sqrt(log(1 + e^z)) */
+} moe_score;
+
+/*
+ * How logits become a routing.
+ *
+ *   s_e   = score of logit z_e
+ *   key_e = s_e + bias_e               the bias (for balance) selects, and enters no weight
+ *   groups of n_experts / n_groups consecutive experts, worth their largest key
+ *           (group_top2 = 0) or the sum of their two largest; the topk_groups worthiest
+ *           take part (lower group on a tie). n_groups = topk_groups = 1: no groups
+ *   sel   = the top_k largest keys, descending (lower expert on a tie)
+ *   w_j   = route_scale * s_sel(j), divided by their sum when renormalize is not 0
+ *
+ * Supported: n_experts <= 512, top_k <= 32, n_groups <= 32 (else MOE_ERR_UNSUPPORTED);
+ * n_experts % n_groups == 0, topk_groups <= n_groups, top_k <= topk_groups * n_experts /
+ * n_groups, route_scale > 0 and finite (else MOE_ERR_INVALID_ARG).
+ */
+typedef struct {
+  int32_t n_experts;
+  int32_t top_k;
+  int32_t n_groups;
+  int32_t topk_groups;
+  int32_t score;       /* moe_score */
+  int32_t group_top2;
+  int32_t renormalize;
+  float route_scale;
+} moe_route_config;
+
+/*
+ *   logits   [T, n_experts] of dtype (moe_value_dtype), device, rows row_stride elements apart
+ *   bias     fp32 [n_experts] device, or NULL
+ *   topk_idx int32 [T, top_k] device (output)
+ *   topk_w   fp32  [T, top_k] device (output)
+ * The selection is that of exact keys: scores that 32 bits cannot tell apart are compared
+ * in 64. An expert whose logit is -infinity is off: it is never selected, has score 0 and
+ * counts for nothing in its group; a slot left without an expert gets index -1 and weight 0
+ * (all of them in a row whose logits are all -infinity). A row with a NaN or +infinite logit,
+ * or with a key that is not finite, gets the placeholder experts 0 .. top_k - 1 with NaN
+ * weights, as in moe_route_noalloc. No scratch, no allocation, no synchronisation; calls are
+ * independent of each other.
+ */
+MOE_API moe_status moe_route(const moe_route_config* cfg, const void* logits, int32_t dtype, int64_t row_stride,
+                             const float* bias, int32_t T, int32_t* topk_idx, float* topk_w, moe_stream_t stream);
+
+/*
+ * Gradient of the logits from the weights' gradient grad_w fp32 [T, top_k], with the selection
+ * topk_idx [T, top_k] held fixed (the bias gets none: it only selects). grad_logits [T, n_experts],
+ * contiguous, of the logits' dtype, may not be the logits; every element is written. Slots whose
+ * index is outside [0, n_experts) (-1: empty) take no part; an expert named twice in a row gets the
+ * sum of its slots' gradients. The groups of cfg play no part. The gradient of a row that moe_route
+ * answered with NaN weights is not defined.
+ */
+MOE_API moe_status moe_route_backward(const moe_route_config* cfg, const float* grad_w, const void* logits,
+                                      int32_t dtype, int64_t row_stride, const int32_t* topk_idx, int32_t T,
+                                      void* grad_logits, moe_stream_t stream);
+
+/*
+ * moe_forward with the caller's routing (moe_route's, or any other): topk_idx int32 [T, k] and
+ * topk_w fp32 [T, k], device, k = the handle's top_k; the weights are used as they are. Index -1
+ * is an empty slot (the token takes fewer experts; its shared experts still run). Any other index
+ * outside [0, n_routed) gives the token a NaN output row, and moe_get_status reports
+ * MOE_ERR_DEVICE. An expert named twice by a token counts twice. Everything after the routing is
+ * moe_forward's; expert-window handles are rejected.
+ */
+MOE_API moe_status moe_forward_routed(moe_handle* h, const void* x, const int32_t* topk_idx, const float* topk_w,
+                                      int32_t T, void* y, moe_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Microscaled 4-bit floating point: quantisation and product
+ * ---------------------------------------------------------------------- */
+
+typedef enum {
+  MOE_FP4_MX = 0, /* MXFP4: E2M1 elements, one E8M0 scale per 32 along K (the layer's format) */
+  MOE_FP4_NV = 1  /* NVFP4: E2M1 elements, one E4M3 scale per 16 along K, and a tensor scale */
+} moe_fp4_format;
+
+/*
+ * Quantise src [rows, cols] (dtype moe_value_dtype, device, rows row_stride elements apart;
+ * cols % 32 == 0) to codes [rows, cols / 2] (element 2j in the low nibble of byte j; 16-byte
+ * aligned) and scales (rows scale_stride bytes apart, cols / 32 or cols / 16 of them; bytes
+ * behind them are not written).
+ *   MXFP4: the rule of moe_quantize_mxfp4.
+ *   NVFP4: sf = the E4M3 nearest to amax / (6 ts), at most 448; an element stands for e2m1 * d with
+ *          d = sf * ts rounded to fp32, and is the nearest such value (ties to even, at most 6 d);
+ *          ts = *tensor_scale (fp32, device, positive), or 1 when NULL. MXFP4 takes NULL.
+ * A block holding NaN or infinity gets the scale format's NaN (0xFF, 0x7F) and zero codes.
+ */
+MOE_API moe_status moe_quantize_fp4(int32_t format, const void* src, int32_t dtype, int64_t rows, int32_t cols,
+                                    int64_t row_stride, const float* tensor_scale, uint8_t* codes, uint8_t* scales,
+                                    int64_t scale_stride, moe_stream_t stream);
+
+/* The values of codes and scales, rounded once to dst [rows, cols] (contiguous, dtype). */
+MOE_API moe_status moe_dequantize_fp4(int32_t format, const uint8_t* codes, const uint8_t* scales, int64_t rows,
+                                      int32_t cols, int64_t scale_stride, const float* tensor_scale, void* dst,
+                                      int32_t dtype, moe_stream_t stream);
+
+/*
+ * y[t, n] = sum_k x[t, k] w[g, n, k] over the values that codes and scales stand for, accumulated
+ * in fp32 and rounded once to y's type.
+ *   x [T, K/2], w [E, N, K/2] codes, 16-byte aligned; K % 32 == 0
+ *   x_scales, w_scales: K/32 or K/16 bytes per row, rows *_scale_stride bytes apart (where base and
+ *          stride are multiples of 16 bytes, or of 8 for MXFP4, a row is read up to the next such
+ *          boundary in one load: the last row must be readable that far)
+ *   x_tensor_scale fp32 [1], w_tensor_scale fp32 [E] (device) or NULL; NVFP4 only
+ *   offsets int32 [E + 1] device: rows offsets[g] .. offsets[g + 1] meet w[g]. Rows in none of
+ *          these ranges (behind the last, in front of the first) are left as they were. Values are
+ *          clamped to [0, T] and to ascending order. NULL: E = 1, every row.
+ *   y [T, N] contiguous, out_dtype (moe_value_dtype)
+ *   status: int32 device word that a wait which ran out sets to 1, or NULL
+ * Limits: T <= 2^22, N and K <= 2^18, E <= 512. No scratch, no allocation, no synchronisation.
+ */
+typedef struct {
+  int32_t format; /* moe_fp4_format */
+  int32_t T, N, K, E;
+  int32_t out_dtype;
+  const uint8_t* x;
+  const uint8_t* x_scales;
+  int64_t x_scale_stride;
+  const float* x_tensor_scale;
+  const uint8_t* w;
+  const uint8_t* w_scales;
+  int64_t w_scale_stride;
+  const float* w_tensor_scale;
+  const int32_t* offsets;
+  void* y;
+  int32_t* status;
+} moe_fp4_product;
+
+MOE_API moe_status moe_fp4_matmul(const moe_fp4_product* p, moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

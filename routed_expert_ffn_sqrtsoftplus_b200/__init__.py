@@ -35,7 +35,14 @@ EXPORTED = ("moe_create", "moe_forward", "moe_forward_host", "moe_get_status", "
             "moe_selftest_wait_timeout", "moe_get_info", "moe_profile_begin", "moe_profile_end",
             "moe_num_kernel_kinds", "moe_kernel_name", "moe_route_noalloc", "moe_quantize_mxfp8",
             "moe_set_hash_table", "moe_forward_hashed", "moe_fill_workspace", "moe_create_ep",
-            "moe_forward_partial", "moe_read_bandwidth", "moe_forward_host_async", "moe_forward_host_wait")
+            "moe_forward_partial", "moe_read_bandwidth", "moe_forward_host_async", "moe_forward_host_wait",
+            "moe_route", "moe_route_backward", "moe_forward_routed", "moe_quantize_fp4", "moe_dequantize_fp4",
+            "moe_fp4_matmul")
+
+SCORES = {"softmax": 0, "sigmoid": 1, "sqrtsoftplus": 2}
+FP4_FORMATS = {"mxfp4": 0, "nvfp4": 1}
+FP4_BLOCK = {"mxfp4": 32, "nvfp4": 16}   # values of K per scale
+_VALUE_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
 
 class MoEError(RuntimeError):
@@ -60,6 +67,19 @@ class _Weights(ctypes.Structure):
 class _Info(ctypes.Structure):
     _fields_ = [("weight_bytes", ctypes.c_uint64), ("workspace_bytes", ctypes.c_uint64),
                 ("num_sms", ctypes.c_int32), ("last_tokens", ctypes.c_int32)]
+
+
+class _RouteConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("n_experts", "top_k", "n_groups", "topk_groups", "score", "group_top2",
+                                             "renormalize")] + [("route_scale", ctypes.c_float)]
+
+
+class _Fp4Product(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("format", "T", "N", "K", "E", "out_dtype")] +
+                [("x", ctypes.c_void_p), ("x_scales", ctypes.c_void_p), ("x_scale_stride", ctypes.c_int64),
+                 ("x_tensor_scale", ctypes.c_void_p), ("w", ctypes.c_void_p), ("w_scales", ctypes.c_void_p),
+                 ("w_scale_stride", ctypes.c_int64)] +
+                [(n, ctypes.c_void_p) for n in ("w_tensor_scale", "offsets", "y", "status")])
 
 
 _lib = None
@@ -102,6 +122,12 @@ def lib() -> ctypes.CDLL:
             "moe_num_kernel_kinds": (I32, []),
             "moe_kernel_name": (ctypes.c_char_p, [I32]),
             "moe_route_noalloc": (I32, [P, P, P, I32, I32, I32, I32, ctypes.c_float, P, P, P]),
+            "moe_route": (I32, [ctypes.POINTER(_RouteConfig), P, I32, I64, P, I32, P, P, P]),
+            "moe_route_backward": (I32, [ctypes.POINTER(_RouteConfig), P, P, I32, I64, P, I32, P, P]),
+            "moe_forward_routed": (I32, [P, P, P, P, I32, P, P]),
+            "moe_quantize_fp4": (I32, [I32, P, I32, I64, I32, I64, P, P, P, I64, P]),
+            "moe_dequantize_fp4": (I32, [I32, P, P, I64, I32, I64, P, P, I32, P]),
+            "moe_fp4_matmul": (I32, [ctypes.POINTER(_Fp4Product), P]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -181,6 +207,275 @@ def read_bandwidth(buf: torch.Tensor, reps: int = 5, stream=None) -> float:
     _check(lib().moe_read_bandwidth(_ptr(buf), buf.numel() * buf.element_size(), reps, _stream(stream),
                                     ctypes.byref(g)), "moe_read_bandwidth")
     return g.value
+
+
+# ------------------------------------------------------------------ operators without a handle
+# With `stream`, the whole call runs on it (its outputs and workspaces belong to it as well).
+def _on_stream(stream):
+    return torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
+
+
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _current(t: torch.Tensor) -> int:
+    return torch._C._cuda_getCurrentRawStream(t.device.index)
+
+
+def _same_device(ref: torch.Tensor, **tensors):
+    for n, t in tensors.items():
+        if t is not None and t.device != ref.device:
+            raise ValueError(f"{n} is on {t.device}, expected {ref.device}")
+
+
+def _rows(t: torch.Tensor, name: str):
+    """A CUDA matrix of a supported value type with contiguous rows: (rows, cols, row stride, dtype code)."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on cuda")
+    code = _VALUE_DTYPES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} must be bfloat16, float16 or float32, got {t.dtype}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have 2 dimensions, got {t.dim()}")
+    r, c = t.shape
+    if c > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    rs = t.stride(0) if r > 1 else c
+    if rs < c:
+        raise ValueError(f"{name} must not have overlapping rows")
+    return r, c, rs, code
+
+
+def _route_config(E, k, n_groups, topk_groups, score, group_score, renormalize, route_scale):
+    if score not in SCORES:
+        raise ValueError(f"score must be one of {tuple(SCORES)}")
+    if group_score not in ("top2", "max"):
+        raise ValueError("group_score must be 'top2' or 'max'")
+    return _RouteConfig(E, k, n_groups, topk_groups, SCORES[score], group_score == "top2", bool(renormalize),
+                        route_scale)
+
+
+def route(logits: torch.Tensor, top_k: int, *, score: str = "softmax", bias: Optional[torch.Tensor] = None,
+          n_groups: int = 1, topk_groups: int = 1, group_score: str = "top2", renormalize: bool = True,
+          route_scale: float = 1.0, topk_idx: Optional[torch.Tensor] = None, topk_w: Optional[torch.Tensor] = None,
+          stream=None):
+    """Routing from logits [T, E] (bfloat16, float16 or float32): (topk_idx int32 [T, k], topk_w fp32 [T, k]).
+
+    The k experts with the largest score + bias, from the topk_groups worthiest of n_groups groups of
+    consecutive experts (worth: the largest key, or with group_score "top2" the sum of the two largest), in
+    descending order, lower expert first on a tie; the weights are the scores without the bias, divided by their
+    sum with ``renormalize``, times route_scale. A logit of -inf takes its expert out; a slot without an expert
+    has index -1 and weight 0. A row that is not finite (NaN or +inf) gets experts 0..k-1 with NaN weights.
+    """
+    if stream is not None:
+        with _on_stream(stream):
+            return route(logits, top_k, score=score, bias=bias, n_groups=n_groups, topk_groups=topk_groups,
+                         group_score=group_score, renormalize=renormalize, route_scale=route_scale,
+                         topk_idx=topk_idx, topk_w=topk_w)
+    T, E, rs, code = _rows(logits, "logits")
+    if bias is not None:
+        _need(bias, "bias", torch.float32, (E,))
+    cfg = _route_config(E, top_k, n_groups, topk_groups, score, group_score, renormalize, route_scale)
+    if topk_idx is None:
+        topk_idx = torch.empty((T, top_k), dtype=torch.int32, device=logits.device)
+    else:
+        _need(topk_idx, "topk_idx", torch.int32, (T, top_k))
+    if topk_w is None:
+        topk_w = torch.empty((T, top_k), dtype=torch.float32, device=logits.device)
+    else:
+        _need(topk_w, "topk_w", torch.float32, (T, top_k))
+    _same_device(logits, bias=bias, topk_idx=topk_idx, topk_w=topk_w)
+    _check(lib().moe_route(cfg, logits.data_ptr(), code, rs, _addr(bias), T, topk_idx.data_ptr(),
+                           topk_w.data_ptr(), _current(logits)), "moe_route")
+    return topk_idx, topk_w
+
+
+def route_backward(grad_w: torch.Tensor, logits: torch.Tensor, topk_idx: torch.Tensor, *, score: str = "softmax",
+                   renormalize: bool = True, route_scale: float = 1.0, out: Optional[torch.Tensor] = None,
+                   stream=None) -> torch.Tensor:
+    """Gradient of the logits [T, E] (in their dtype) from that of route()'s weights, the selection held fixed."""
+    if stream is not None:
+        with _on_stream(stream):
+            return route_backward(grad_w, logits, topk_idx, score=score, renormalize=renormalize,
+                                  route_scale=route_scale, out=out)
+    T, E, rs, code = _rows(logits, "logits")
+    k = topk_idx.shape[-1]
+    _need(topk_idx, "topk_idx", torch.int32, (T, k))
+    _need(grad_w, "grad_w", torch.float32, (T, k))
+    cfg = _route_config(E, k, 1, 1, score, "max", renormalize, route_scale)
+    if out is None:
+        out = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
+    else:
+        _need(out, "out", logits.dtype, (T, E))
+    _same_device(logits, grad_w=grad_w, topk_idx=topk_idx, out=out)
+    _check(lib().moe_route_backward(cfg, grad_w.data_ptr(), logits.data_ptr(), code, rs, topk_idx.data_ptr(), T,
+                                    out.data_ptr(), _current(logits)), "moe_route_backward")
+    return out
+
+
+def _fp4_format(fmt: str) -> int:
+    if fmt not in FP4_FORMATS:
+        raise ValueError(f"fmt must be one of {tuple(FP4_FORMATS)}")
+    return FP4_FORMATS[fmt]
+
+
+def _tensor_scale(t: Optional[torch.Tensor], name: str, fmt: str, n: int):
+    if t is None:
+        return None
+    if fmt != "nvfp4":
+        raise ValueError(f"{name} is for nvfp4")
+    if t.numel() != n:
+        raise ValueError(f"{name} must hold {n} value(s), got {t.numel()}")
+    _need(t, name, torch.float32)
+    return t.data_ptr()
+
+
+def quantize_fp4(x: torch.Tensor, fmt: str, tensor_scale: Optional[torch.Tensor] = None, stream=None):
+    """x [rows, K] (bfloat16, float16 or float32; K % 32 == 0) -> (codes uint8 [rows, K/2], scales uint8).
+
+    fmt "mxfp4": scales E8M0 [rows, K/32], the rule of quantize_mxfp4. fmt "nvfp4": scales E4M3 [rows, K/16],
+    relative to tensor_scale (fp32, one value; 1 when None). Element 2j is the low nibble of byte j.
+    """
+    if stream is not None:
+        with _on_stream(stream):
+            return quantize_fp4(x, fmt, tensor_scale)
+    f = _fp4_format(fmt)
+    rows, K, rs, code = _rows(x, "x")
+    if K % 32 != 0:
+        raise ValueError(f"x must have a multiple of 32 columns, got {K}")
+    ts = _tensor_scale(tensor_scale, "tensor_scale", fmt, 1)
+    _same_device(x, tensor_scale=tensor_scale)
+    sc = K // FP4_BLOCK[fmt]
+    codes = torch.empty((rows, K // 2), dtype=torch.uint8, device=x.device)
+    scales = torch.empty((rows, sc), dtype=torch.uint8, device=x.device)
+    _check(lib().moe_quantize_fp4(f, x.data_ptr(), code, rows, K, rs, ts, codes.data_ptr(), scales.data_ptr(), sc,
+                                  _current(x)), "moe_quantize_fp4")
+    return codes, scales
+
+
+def dequantize_fp4(codes: torch.Tensor, scales: torch.Tensor, fmt: str, tensor_scale: Optional[torch.Tensor] = None,
+                   dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
+    """The values [rows, K] that codes [rows, K/2] and scales stand for, rounded once to dtype."""
+    if stream is not None:
+        with _on_stream(stream):
+            return dequantize_fp4(codes, scales, fmt, tensor_scale, dtype)
+    f = _fp4_format(fmt)
+    if dtype not in _VALUE_DTYPES:
+        raise ValueError(f"dtype must be bfloat16, float16 or float32, got {dtype}")
+    if codes.dim() != 2:
+        raise ValueError(f"codes must have 2 dimensions, got {codes.dim()}")
+    rows, K = codes.shape[0], codes.shape[1] * 2
+    _need(codes, "codes", torch.uint8)
+    if K % 32 != 0:
+        raise ValueError(f"codes must have a multiple of 16 columns, got {codes.shape[1]}")
+    _need(scales, "scales", torch.uint8, (rows, K // FP4_BLOCK[fmt]))
+    ts = _tensor_scale(tensor_scale, "tensor_scale", fmt, 1)
+    _same_device(codes, scales=scales, tensor_scale=tensor_scale)
+    out = torch.empty((rows, K), dtype=dtype, device=codes.device)
+    _check(lib().moe_dequantize_fp4(f, codes.data_ptr(), scales.data_ptr(), rows, K, scales.shape[1], ts,
+                                    out.data_ptr(), _VALUE_DTYPES[dtype], _current(codes)), "moe_dequantize_fp4")
+    return out
+
+
+def _fp4_weights(w, w_scales, fmt, K, offsets):
+    """(E, N) of w [N, K/2] or, with offsets, [E, N, K/2]."""
+    lead = w.shape[:-1]
+    if w.dim() != (2 if offsets is None else 3) or w.shape[-1] * 2 != K:
+        raise ValueError(f"w must be [{'' if offsets is None else 'E, '}N, {K // 2}], got {tuple(w.shape)}")
+    _need(w, "w", torch.uint8)
+    _need(w_scales, "w_scales", torch.uint8, tuple(lead) + (K // FP4_BLOCK[fmt],))
+    E = 1 if offsets is None else w.shape[0]
+    if offsets is not None:
+        _need(offsets, "offsets", torch.int32, (E + 1,))
+    return E, lead[-1]
+
+
+def _fp4_out(x, T, N, out, out_dtype):
+    if out is None:
+        return torch.empty((T, N), dtype=out_dtype, device=x.device)
+    if out.dtype not in _VALUE_DTYPES:
+        raise ValueError(f"out must be bfloat16, float16 or float32, got {out.dtype}")
+    _need(out, "out", out.dtype, (T, N))
+    return out
+
+
+def _fp4_product(f, x, x_scales, xss, x_ts, w, w_scales, w_ts, offsets, out, T, N, K, E, status):
+    p = _Fp4Product(f, T, N, K, E, _VALUE_DTYPES[out.dtype], x.data_ptr(), x_scales.data_ptr(), xss, x_ts,
+                    w.data_ptr(), w_scales.data_ptr(), w_scales.shape[-1], w_ts, _addr(offsets), out.data_ptr(),
+                    _addr(status))
+    _check(lib().moe_fp4_matmul(p, _current(x)), "moe_fp4_matmul")
+    return out
+
+
+def fp4_matmul(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor, fmt: str, *,
+               x_tensor_scale: Optional[torch.Tensor] = None, w_tensor_scale: Optional[torch.Tensor] = None,
+               offsets: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+               out_dtype: torch.dtype = torch.bfloat16, status: Optional[torch.Tensor] = None,
+               stream=None) -> torch.Tensor:
+    """y [T, N] = x w^T over the values of FP4 codes (quantize_fp4's): x [T, K/2], w [N, K/2].
+
+    With offsets (int32 [E + 1], on the device) w is [E, N, K/2] and rows offsets[g] .. offsets[g + 1] of x meet
+    w[g]; rows in no range are left as they were in ``out`` (not set where out is None). w_tensor_scale: one value
+    per expert. status: int32 [1], set to 1 if a device-side wait ran out.
+    """
+    if stream is not None:
+        with _on_stream(stream):
+            return fp4_matmul(x, x_scales, w, w_scales, fmt, x_tensor_scale=x_tensor_scale,
+                              w_tensor_scale=w_tensor_scale, offsets=offsets, out=out, out_dtype=out_dtype,
+                              status=status)
+    f = _fp4_format(fmt)
+    if x.dim() != 2:
+        raise ValueError(f"x must have 2 dimensions, got {x.dim()}")
+    if out is None and out_dtype not in _VALUE_DTYPES:
+        raise ValueError(f"out_dtype must be bfloat16, float16 or float32, got {out_dtype}")
+    T, K = x.shape[0], x.shape[1] * 2
+    _need(x, "x", torch.uint8)
+    if K % 32 != 0:
+        raise ValueError(f"x must have a multiple of 16 columns, got {x.shape[1]}")
+    _need(x_scales, "x_scales", torch.uint8, (T, K // FP4_BLOCK[fmt]))
+    E, N = _fp4_weights(w, w_scales, fmt, K, offsets)
+    x_ts = _tensor_scale(x_tensor_scale, "x_tensor_scale", fmt, 1)
+    w_ts = _tensor_scale(w_tensor_scale, "w_tensor_scale", fmt, E)
+    out = _fp4_out(x, T, N, out, out_dtype)
+    if status is not None:
+        _need(status, "status", torch.int32, (1,))
+    _same_device(x, x_scales=x_scales, w=w, w_scales=w_scales, x_tensor_scale=x_tensor_scale,
+                 w_tensor_scale=w_tensor_scale, offsets=offsets, out=out, status=status)
+    return _fp4_product(f, x, x_scales, x_scales.shape[1], x_ts, w, w_scales, w_ts, offsets, out, T, N, K, E, status)
+
+
+def fp4_linear(x: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor, fmt: str, *,
+               x_tensor_scale: Optional[torch.Tensor] = None, w_tensor_scale: Optional[torch.Tensor] = None,
+               offsets: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+               status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """y = x w^T with x [T, K] (bfloat16, float16 or float32) quantised to fmt first, then fp4_matmul.
+
+    w, w_scales, the tensor scales, offsets, out and status as there; y has x's dtype unless out says otherwise.
+    """
+    if stream is not None:
+        with _on_stream(stream):
+            return fp4_linear(x, w, w_scales, fmt, x_tensor_scale=x_tensor_scale, w_tensor_scale=w_tensor_scale,
+                              offsets=offsets, out=out, status=status)
+    f = _fp4_format(fmt)
+    T, K, rs, code = _rows(x, "x")
+    if K % 32 != 0:
+        raise ValueError(f"x must have a multiple of 32 columns, got {K}")
+    E, N = _fp4_weights(w, w_scales, fmt, K, offsets)
+    x_ts = _tensor_scale(x_tensor_scale, "x_tensor_scale", fmt, 1)
+    w_ts = _tensor_scale(w_tensor_scale, "w_tensor_scale", fmt, E)
+    out = _fp4_out(x, T, N, out, x.dtype)
+    if status is not None:
+        _need(status, "status", torch.int32, (1,))
+    _same_device(x, w=w, w_scales=w_scales, x_tensor_scale=x_tensor_scale, w_tensor_scale=w_tensor_scale,
+                 offsets=offsets, out=out, status=status)
+    # one workspace: the codes, then the scales in rows padded to 16 bytes (read in whole vectors)
+    ss = (K // FP4_BLOCK[fmt] + 15) // 16 * 16
+    codes = torch.empty(T * (K // 2 + ss), dtype=torch.uint8, device=x.device)
+    scales = codes[T * (K // 2):]
+    _check(lib().moe_quantize_fp4(f, x.data_ptr(), code, T, K, rs, x_ts, codes.data_ptr(), scales.data_ptr(), ss,
+                                  _current(x)), "moe_quantize_fp4")
+    return _fp4_product(f, codes, scales, ss, x_ts, w, w_scales, w_ts, offsets, out, T, N, K, E, status)
 
 
 class MoELayer:
@@ -303,6 +598,27 @@ class MoELayer:
             _need(topk_w, "topk_w", torch.float32, (T, self.top_k))
         _check(lib().moe_forward_hashed(self._h, _ptr(x), _ptr(token_ids), T, _ptr(out), _ptr(topk_idx),
                                         _ptr(topk_w), _stream(stream)), "moe_forward_hashed")
+        return out
+
+    def forward_routed(self, x: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tensor,
+                       out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """The layer with a given routing (route()'s, or any other): experts topk_idx int32 [T, top_k], -1 for an
+        empty slot, with weights topk_w fp32 [T, top_k] as they are."""
+        if stream is not None:
+            with _on_stream(stream):
+                return self.forward_routed(x, topk_idx, topk_w, out)
+        T = x.shape[0]
+        _need(x, "x", torch.bfloat16, (T, self.hidden))
+        _need(topk_idx, "topk_idx", torch.int32, (T, self.top_k))
+        _need(topk_w, "topk_w", torch.float32, (T, self.top_k))
+        if out is None:
+            out = torch.empty_like(x)
+        _need(out, "out", torch.bfloat16, (T, self.hidden))
+        for n, t in (("x", x), ("topk_idx", topk_idx), ("topk_w", topk_w), ("out", out)):
+            if t.device != self.device:
+                raise ValueError(f"{n} is on {t.device}, the layer on {self.device}")
+        _check(lib().moe_forward_routed(self._h, _ptr(x), _ptr(topk_idx), _ptr(topk_w), T, _ptr(out),
+                                        _stream(None)), "moe_forward_routed")
         return out
 
     def forward_with_routing(self, x: torch.Tensor, stream=None):

@@ -71,7 +71,8 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 const char* kKernelNames[kKNumKinds] = {"router_logits", "router_gemm",  "topk_refine", "perm_count",
                                         "perm_scan",     "perm_scatter", "gather_rows", "gemm_gateup",
                                         "gemm_down",     "combine",      "quant_x",     "gemm_gateup_mx",
-                                        "gemm_down_mx",  "swiglu_reduce", "hash_route",  "gemm_fused"};
+                                        "gemm_down_mx",  "swiglu_reduce", "hash_route",  "gemm_fused",
+                                        "take_routing"};
 
 // 2-D tensor map, box of box_cols x box_rows elements, 128-byte swizzle unless stated.
 bool make_tmap(CUtensorMap* m, const void* ptr, CUtensorMapDataType dt, uint64_t rows, uint64_t cols,
@@ -88,6 +89,14 @@ bool make_tmap(CUtensorMap* m, const void* ptr, CUtensorMapDataType dt, uint64_t
 }
 
 }  // namespace
+
+namespace moe {
+
+bool encode_tmap_bytes(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t row_bytes, uint32_t box_rows) {
+  return make_tmap(m, ptr, CU_TENSOR_MAP_DATA_TYPE_UINT8, rows, row_bytes, row_bytes, 128, box_rows);
+}
+
+}  // namespace moe
 
 struct moe_handle {
   moe_config cfg{};
@@ -524,8 +533,10 @@ namespace {
 // handle's table instead of the learned router and top-k.
 // y_f32: y is fp32 [T, H] and receives this instance's partial output (its expert
 // window's slots, plus the shared experts it holds), else BF16 [T, H].
+// given_idx / given_w != nullptr: the caller's routing takes the place of both.
 moe_status forward_impl(moe_handle* h, const void* x, const int32_t* token_ids, int32_t T, void* y, bool y_f32,
-                        int32_t* topk_idx, float* topk_w, moe_stream_t stream) {
+                        int32_t* topk_idx, float* topk_w, moe_stream_t stream, const int32_t* given_idx = nullptr,
+                        const float* given_w = nullptr) {
   if (h == nullptr) return MOE_ERR_INVALID_ARG;
   if (T < 0 || T > h->cfg.max_tokens) return MOE_ERR_INVALID_ARG;
   if (T == 0) {
@@ -578,7 +589,11 @@ moe_status forward_impl(moe_handle* h, const void* x, const int32_t* token_ids, 
   if (!make_tmap_bf16(&tm_x, x, static_cast<uint64_t>(T), static_cast<uint64_t>(H), 32)) return MOE_ERR_CUDA;
 
   // 1-2. router logits (+ bias), scores, top-k, weights
-  if (token_ids != nullptr) {
+  if (given_idx != nullptr) {
+    h->prof_mark(kKTakeRouting, s);
+    MOE_TRY_CUDA(launch_take_routing(given_idx, given_w, T, k, E, h->idx, h->wts, h->status, s));
+    h->prof_done(s);
+  } else if (token_ids != nullptr) {
     h->prof_mark(kKHashRoute, s);
     MOE_TRY_CUDA(launch_hash_route(x, h->wg, h->bias, h->hash_table, token_ids, T, H, E, k, h->hash_vocab,
                                    c.route_scale, h->idx, h->wts, h->status, s));
@@ -636,7 +651,7 @@ moe_status forward_impl(moe_handle* h, const void* x, const int32_t* token_ids, 
     MOE_TRY_CUDA(launch_gemm_down(h->tm_wg, tm_x, a, kBnLarge, nt < h->num_sms ? nt : h->num_sms, s));
     h->prof_done(s);
   }
-  if (token_ids == nullptr && T > kSmallRouterMaxTokens) {
+  if (given_idx == nullptr && token_ids == nullptr && T > kSmallRouterMaxTokens) {
     // scores, top-k with exact refinement of the near-tie candidates, weights
     h->prof_mark(kKTopk, s);
     if (T <= kTopkCtaMaxTokens) {
@@ -998,6 +1013,18 @@ moe_status moe_forward_hashed(moe_handle* h, const void* x, const int32_t* token
   }
   if (h->e_local != h->cfg.n_routed) return MOE_ERR_INVALID_ARG;
   return forward_impl(h, x, token_ids, T, y, false, topk_idx, topk_w, stream);
+}
+
+moe_status moe_forward_routed(moe_handle* h, const void* x, const int32_t* topk_idx, const float* topk_w, int32_t T,
+                              void* y, moe_stream_t stream) {
+  if (h == nullptr || h->e_local != h->cfg.n_routed) return MOE_ERR_INVALID_ARG;
+  if (T > 0) {
+    if (topk_idx == nullptr || topk_w == nullptr) return MOE_ERR_INVALID_ARG;
+    int cur = -1;
+    if (cudaGetDevice(&cur) != cudaSuccess || cur != h->device) return MOE_ERR_INVALID_ARG;
+    if (!device_pointer_on(topk_idx, h->device) || !device_pointer_on(topk_w, h->device)) return MOE_ERR_INVALID_ARG;
+  }
+  return forward_impl(h, x, nullptr, T, y, false, nullptr, nullptr, stream, topk_idx, topk_w);
 }
 
 moe_status moe_forward_host(moe_handle* h, const void* x_host, int32_t T, void* y_host, int32_t* topk_idx_host,

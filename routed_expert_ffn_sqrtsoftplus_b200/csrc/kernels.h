@@ -82,6 +82,7 @@ enum KernelKind {
   kKSwigluReduce,
   kKHashRoute,
   kKGemmFused,
+  kKTakeRouting,
   kKNumKinds
 };
 
@@ -301,6 +302,77 @@ cudaError_t launch_repack_w13(const void* w1, const void* w3, const void* sh1, c
 // ---- read-only streaming (roofline denominator): reads bytes / 32 KiB chunks of buf
 cudaError_t launch_stream_read(const void* buf, size_t bytes, int grid, int* status, unsigned long long timeout_ns,
                                cudaStream_t s);
+
+// ---- routing from given logits (route.cu)
+constexpr int kValBf16 = 0, kValFp16 = 1, kValFp32 = 2;  // moe_value_dtype
+constexpr int kScoreSoftmax = 0, kScoreSigmoid = 1, kScoreSqrtSoftplus = 2;  // moe_score
+struct RouteArgs {
+  const void* logits;           // [T, E], rows row_stride elements apart
+  int dtype;
+  int64_t row_stride;
+  const float* bias;            // [E] added to the keys, or null
+  int T, E, k, n_groups, topk_groups;
+  int score, group_sum2, renorm;
+  float scale;
+  int32_t* idx;                 // [T, k]
+  float* w;                     // [T, k]
+};
+cudaError_t launch_route(const RouteArgs& r, cudaStream_t s);
+struct RouteGradArgs {
+  const float* grad_w;          // [T, k]
+  const void* logits;
+  int dtype;                    // of the logits and of out
+  int64_t row_stride;
+  const int32_t* idx;           // [T, k]
+  int T, E, k;
+  int score, renorm;
+  float scale;
+  void* out;                    // [T, E]
+};
+cudaError_t launch_route_grad(const RouteGradArgs& r, cudaStream_t s);
+// A caller's routing [T, k] into the layer's idx and w (checked against [0, E); -1: an empty slot).
+cudaError_t launch_take_routing(const int32_t* idx_in, const float* w_in, int T, int k, int E, int32_t* idx, float* w,
+                                int* status, cudaStream_t s);
+
+// 2-D map over bytes: rows of row_bytes (a multiple of 16), boxes of 128 bytes x box_rows, 128-byte swizzle.
+bool encode_tmap_bytes(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t row_bytes, uint32_t box_rows);
+
+// ---- microscaled FP4 (fp4.cu, gemm_fp4.cu)
+constexpr int kFp4Mx = 0, kFp4Nv = 1;  // moe_fp4_format
+// [rows, cols] values (rows row_stride elements apart) -> codes [rows, cols / 2] and scales, rows
+// scale_stride bytes apart.
+cudaError_t launch_quantize_fp4(int format, const void* src, int dtype, int64_t rows, int cols, int64_t row_stride,
+                                const float* tensor_scale, uint8_t* codes, uint8_t* scales, int64_t scale_stride,
+                                cudaStream_t s);
+cudaError_t launch_dequantize_fp4(int format, const uint8_t* codes, const uint8_t* scales, int64_t rows, int cols,
+                                  int64_t scale_stride, const float* tensor_scale, void* dst, int dtype,
+                                  cudaStream_t s);
+// y[t, n] = alpha sum_k x[t, k] w[g(t), n, k]; see gemm_fp4.cu
+struct Fp4GemmArgs {
+  const uint8_t* xs;            // scales of x, rows xs_stride bytes apart
+  const uint8_t* ws;            // scales of w, rows ws_stride bytes apart
+  int64_t xs_stride, ws_stride;
+  int sf_cols;                  // scales per row: K / 32 or K / 16
+  const float* x_ts;            // tensor scale of x, or null
+  const float* w_ts;            // tensor scale per expert, or null
+  const int32_t* offsets;       // device [E + 1], or null (E = 1, all T rows)
+  int T, N, E;
+  int num_kb;                   // K blocks of 256
+  void* out;                    // [T, N]
+  int out_dtype;
+  int m_tiles;                  // tiles of w rows per expert
+  int splits;                   // CTAs of a cluster that share a tile's K
+  int* status;
+  unsigned long long timeout_ns;
+};
+struct Fp4Plan {
+  int halves;                   // 128-row halves of w per tile
+  int bn;                       // token rows per tile
+  int splits;
+};
+Fp4Plan fp4_plan(int T, int N, int E, int num_kb, int num_sms);
+cudaError_t launch_gemm_fp4(int format, const CUtensorMap& tm_w, const CUtensorMap& tm_x, const Fp4GemmArgs& a,
+                            const Fp4Plan& p, int num_sms, cudaStream_t s);
 
 // ---- self test
 cudaError_t launch_wait_timeout_probe(int* status, unsigned long long timeout_ns, cudaStream_t s);

@@ -1,0 +1,204 @@
+// Entry points of the operators that need no handle: routing from logits and its gradient, and
+// the microscaled FP4 quantisers and product. Arguments are checked before anything is enqueued.
+#include <cmath>
+#include <initializer_list>
+
+#include "../../include/moe.h"
+#include "common.cuh"
+#include "kernels.h"
+
+using namespace moe;
+
+namespace {
+
+constexpr unsigned long long kWaitNs = 2000000000ull;  // limit of every device-side wait
+
+cudaStream_t as_stream(moe_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
+
+bool aligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+int value_bytes(int32_t dtype) {
+  return dtype == MOE_VAL_FP32 ? 4 : dtype == MOE_VAL_BF16 || dtype == MOE_VAL_FP16 ? 2 : 0;
+}
+
+// MOE_OK when every given pointer is memory of the current device.
+moe_status on_device(std::initializer_list<const void*> ptrs) {
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    return MOE_ERR_CUDA;
+  }
+  for (const void* p : ptrs)
+    if (p != nullptr && !device_pointer_on(p, dev)) return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
+moe_status launched(cudaError_t e) {
+  if (e == cudaSuccess) return MOE_OK;
+  cudaGetLastError();
+  return MOE_ERR_CUDA;
+}
+
+moe_status check_route(const moe_route_config* c) {
+  if (c == nullptr) return MOE_ERR_INVALID_ARG;
+  if (c->score < MOE_SCORE_SOFTMAX || c->score > MOE_SCORE_SQRTSOFTPLUS) return MOE_ERR_INVALID_ARG;
+  if (!(c->route_scale > 0.f) || !std::isfinite(c->route_scale)) return MOE_ERR_INVALID_ARG;
+  if (c->n_experts < 1 || c->top_k < 1 || c->n_groups < 1 || c->topk_groups < 1) return MOE_ERR_INVALID_ARG;
+  if (c->topk_groups > c->n_groups || c->n_experts % c->n_groups != 0) return MOE_ERR_INVALID_ARG;
+  if (c->top_k > c->topk_groups * (c->n_experts / c->n_groups)) return MOE_ERR_INVALID_ARG;
+  if (c->n_experts > 512 || c->top_k > 32 || c->n_groups > 32) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+bool fp4_format_ok(int32_t f) { return f == MOE_FP4_MX || f == MOE_FP4_NV; }
+
+}  // namespace
+
+extern "C" {
+
+moe_status moe_route(const moe_route_config* cfg, const void* logits, int32_t dtype, int64_t row_stride,
+                     const float* bias, int32_t T, int32_t* topk_idx, float* topk_w, moe_stream_t stream) {
+  moe_status st = check_route(cfg);
+  if (st != MOE_OK) return st;
+  const int vb = value_bytes(dtype);
+  if (vb == 0 || T < 0 || row_stride < cfg->n_experts) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (logits == nullptr || topk_idx == nullptr || topk_w == nullptr) return MOE_ERR_INVALID_ARG;
+  if (!aligned(logits, vb) || !aligned(bias, 4) || !aligned(topk_idx, 4) || !aligned(topk_w, 4))
+    return MOE_ERR_INVALID_ARG;
+  if ((st = on_device({logits, bias, topk_idx, topk_w})) != MOE_OK) return st;
+  RouteArgs r{};
+  r.logits = logits;
+  r.dtype = dtype;
+  r.row_stride = row_stride;
+  r.bias = bias;
+  r.T = T;
+  r.E = cfg->n_experts;
+  r.k = cfg->top_k;
+  r.n_groups = cfg->n_groups;
+  r.topk_groups = cfg->topk_groups;
+  r.score = cfg->score;
+  r.group_sum2 = cfg->group_top2 != 0;
+  r.renorm = cfg->renormalize != 0;
+  r.scale = cfg->route_scale;
+  r.idx = topk_idx;
+  r.w = topk_w;
+  return launched(launch_route(r, as_stream(stream)));
+}
+
+moe_status moe_route_backward(const moe_route_config* cfg, const float* grad_w, const void* logits, int32_t dtype,
+                              int64_t row_stride, const int32_t* topk_idx, int32_t T, void* grad_logits,
+                              moe_stream_t stream) {
+  moe_status st = check_route(cfg);
+  if (st != MOE_OK) return st;
+  const int vb = value_bytes(dtype);
+  if (vb == 0 || T < 0 || row_stride < cfg->n_experts) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (grad_w == nullptr || logits == nullptr || topk_idx == nullptr || grad_logits == nullptr || grad_logits == logits)
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned(logits, vb) || !aligned(grad_logits, vb) || !aligned(topk_idx, 4) || !aligned(grad_w, 4))
+    return MOE_ERR_INVALID_ARG;
+  if ((st = on_device({grad_w, logits, topk_idx, grad_logits})) != MOE_OK) return st;
+  RouteGradArgs r{};
+  r.grad_w = grad_w;
+  r.logits = logits;
+  r.dtype = dtype;
+  r.row_stride = row_stride;
+  r.idx = topk_idx;
+  r.T = T;
+  r.E = cfg->n_experts;
+  r.k = cfg->top_k;
+  r.score = cfg->score;
+  r.renorm = cfg->renormalize != 0;
+  r.scale = cfg->route_scale;
+  r.out = grad_logits;
+  return launched(launch_route_grad(r, as_stream(stream)));
+}
+
+moe_status moe_quantize_fp4(int32_t format, const void* src, int32_t dtype, int64_t rows, int32_t cols,
+                            int64_t row_stride, const float* tensor_scale, uint8_t* codes, uint8_t* scales,
+                            int64_t scale_stride, moe_stream_t stream) {
+  const int vb = value_bytes(dtype);
+  if (!fp4_format_ok(format) || vb == 0 || rows < 0 || cols <= 0 || cols % 32 != 0 || row_stride < cols)
+    return MOE_ERR_INVALID_ARG;
+  if (scale_stride < cols / (format == MOE_FP4_NV ? 16 : 32)) return MOE_ERR_INVALID_ARG;
+  if (format == MOE_FP4_MX && tensor_scale != nullptr) return MOE_ERR_INVALID_ARG;
+  if (rows > (int64_t(1) << 38) / cols) return MOE_ERR_UNSUPPORTED;
+  if (rows == 0) return MOE_OK;
+  if (src == nullptr || codes == nullptr || scales == nullptr) return MOE_ERR_INVALID_ARG;
+  if (!aligned(src, vb) || !aligned(codes, 16) || !aligned(tensor_scale, 4)) return MOE_ERR_INVALID_ARG;
+  const moe_status st = on_device({src, tensor_scale, codes, scales});
+  if (st != MOE_OK) return st;
+  return launched(launch_quantize_fp4(format, src, dtype, rows, cols, row_stride, tensor_scale, codes, scales,
+                                      scale_stride, as_stream(stream)));
+}
+
+moe_status moe_dequantize_fp4(int32_t format, const uint8_t* codes, const uint8_t* scales, int64_t rows, int32_t cols,
+                              int64_t scale_stride, const float* tensor_scale, void* dst, int32_t dtype,
+                              moe_stream_t stream) {
+  const int vb = value_bytes(dtype);
+  if (!fp4_format_ok(format) || vb == 0 || rows < 0 || cols <= 0 || cols % 32 != 0) return MOE_ERR_INVALID_ARG;
+  if (scale_stride < cols / (format == MOE_FP4_NV ? 16 : 32)) return MOE_ERR_INVALID_ARG;
+  if (format == MOE_FP4_MX && tensor_scale != nullptr) return MOE_ERR_INVALID_ARG;
+  if (rows > (int64_t(1) << 38) / cols) return MOE_ERR_UNSUPPORTED;
+  if (rows == 0) return MOE_OK;
+  if (codes == nullptr || scales == nullptr || dst == nullptr) return MOE_ERR_INVALID_ARG;
+  if (!aligned(codes, 16) || !aligned(dst, vb) || !aligned(tensor_scale, 4)) return MOE_ERR_INVALID_ARG;
+  const moe_status st = on_device({codes, scales, tensor_scale, dst});
+  if (st != MOE_OK) return st;
+  return launched(launch_dequantize_fp4(format, codes, scales, rows, cols, scale_stride, tensor_scale, dst, dtype,
+                                        as_stream(stream)));
+}
+
+moe_status moe_fp4_matmul(const moe_fp4_product* p, moe_stream_t stream) {
+  if (p == nullptr || !fp4_format_ok(p->format)) return MOE_ERR_INVALID_ARG;
+  if (p->T < 0 || p->N < 1 || p->K < 1 || p->E < 1 || p->K % 32 != 0 || value_bytes(p->out_dtype) == 0)
+    return MOE_ERR_INVALID_ARG;
+  if (p->offsets == nullptr && p->E != 1) return MOE_ERR_INVALID_ARG;
+  const int cols = p->K / (p->format == MOE_FP4_NV ? 16 : 32);
+  if (p->x_scale_stride < cols || p->w_scale_stride < cols) return MOE_ERR_INVALID_ARG;
+  if (p->format == MOE_FP4_MX && (p->x_tensor_scale != nullptr || p->w_tensor_scale != nullptr))
+    return MOE_ERR_INVALID_ARG;
+  if (p->T > 1 << 22 || p->N > 1 << 18 || p->K > 1 << 18 || p->E > 512) return MOE_ERR_UNSUPPORTED;
+  if (p->T == 0) return MOE_OK;
+  if (p->x == nullptr || p->x_scales == nullptr || p->w == nullptr || p->w_scales == nullptr || p->y == nullptr)
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned(p->x, 16) || !aligned(p->w, 16) || !aligned(p->y, value_bytes(p->out_dtype)) ||
+      !aligned(p->offsets, 4) || !aligned(p->x_tensor_scale, 4) || !aligned(p->w_tensor_scale, 4) ||
+      !aligned(p->status, 4))
+    return MOE_ERR_INVALID_ARG;
+  const moe_status st = on_device({p->x, p->x_scales, p->w, p->w_scales, p->y, p->offsets, p->x_tensor_scale,
+                                   p->w_tensor_scale, p->status});
+  if (st != MOE_OK) return st;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return launched(cudaErrorInvalidDevice);
+  Fp4GemmArgs a{};
+  a.xs = p->x_scales;
+  a.ws = p->w_scales;
+  a.xs_stride = p->x_scale_stride;
+  a.ws_stride = p->w_scale_stride;
+  a.sf_cols = cols;
+  a.x_ts = p->x_tensor_scale;
+  a.w_ts = p->w_tensor_scale;
+  a.offsets = p->offsets;
+  a.T = p->T;
+  a.N = p->N;
+  a.E = p->E;
+  a.num_kb = (p->K + 255) / 256;
+  a.out = p->y;
+  a.out_dtype = p->out_dtype;
+  a.status = p->status;
+  a.timeout_ns = kWaitNs;
+  const Fp4Plan plan = fp4_plan(p->T, p->N, p->E, a.num_kb, sms);
+  a.splits = plan.splits;
+  a.m_tiles = (p->N + 128 * plan.halves - 1) / (128 * plan.halves);
+  CUtensorMap tw, tx;
+  if (!encode_tmap_bytes(&tw, p->w, static_cast<uint64_t>(p->E) * p->N, p->K / 2, 128 * plan.halves) ||
+      !encode_tmap_bytes(&tx, p->x, p->T, p->K / 2, 32))
+    return MOE_ERR_CUDA;
+  return launched(launch_gemm_fp4(p->format, tw, tx, a, plan, sms, as_stream(stream)));
+}
+
+}  // extern "C"

@@ -45,7 +45,8 @@ __device__ __forceinline__ int full_seg_tiles(int n, int bn, bool hp) {
 
 // Expert windows (expert parallelism): this layer instance holds routed experts
 // [e_begin, e_begin + E) of e_global; a slot whose expert lies outside the window
-// belongs to another instance and is skipped, one outside [0, e_global) is an error.
+// belongs to another instance and is skipped, as is -1 (an empty slot of a caller's
+// routing); any other outside [0, e_global) is an error.
 __global__ void __launch_bounds__(256)
     perm_count_kernel(const int32_t* __restrict__ idx, int nslots, int E, int e_begin, int e_global,
                       int32_t* __restrict__ chunk_cnt, int* status) {
@@ -57,7 +58,7 @@ __global__ void __launch_bounds__(256)
   for (int s = base + threadIdx.x; s < end; s += blockDim.x) {
     const int g = idx[s];
     const int e = g - e_begin;
-    if (g < 0 || g >= e_global)
+    if (g < -1 || g >= e_global)  // -1: an empty slot of a caller's routing
       report_status(status, kStatusDevice);
     else if (e >= 0 && e < E)
       atomicAdd(&hist[e], 1);
@@ -124,7 +125,7 @@ __global__ void __launch_bounds__(1024) perm_scan_kernel(ScanArgs a, int fused, 
       const int g = idx[s];
       const int e = g - a.e_begin;
       const bool mine = g >= 0 && g < a.e_global && e >= 0 && e < a.E;
-      if (g < 0 || g >= a.e_global) report_status(status, kStatusDevice);
+      if (g < -1 || g >= a.e_global) report_status(status, kStatusDevice);
       if (mine) atomicAdd(&cnt_s[e], 1);
       slot_e[s] = mine ? e : -1;  // kept for the scatter below (no second pass over global memory)
     }

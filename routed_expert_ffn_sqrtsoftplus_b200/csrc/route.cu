@@ -1,0 +1,569 @@
+// Routing from given logits, and its gradient.
+//
+//   s_e = softmax(z)_e | 1 / (1 + e^-z_e) | sqrt(log(1 + e^z_e))
+//   selection by the keys s_e + b_e: the k largest, lower expert first on a tie, from
+//   the topk_groups worthiest of G groups of E / G consecutive experts (worth: the
+//   group's largest key, or the sum of its two largest; lower group first on a tie)
+//   w_j = scale * s_j, or scale * s_j / sum of the selected s
+// An expert whose logit is -inf is off. A slot that finds no expert gets -1 and
+// weight 0. A row with NaN or +inf logits, or keys that are not finite, gets the
+// placeholder experts 0..k-1 with NaN weights.
+//
+// One warp per row: the row is read once and kept in registers, lane l holding the
+// consecutive experts l * EPL + i, so the lowest expert of a tie sits in the lowest
+// lane. The selection takes k rounds of a warp maximum over order-preserving 32-bit
+// keys (redux.sync).
+//
+// Exactness. Without a bias the three scores grow with the logit, so the logits
+// themselves are the keys and the selection is exact. With a bias, or where a group is
+// worth the sum of two scores, keys are 32-bit sums with an error below kKeyTol; a row
+// in which two neighbours of the selection are nearer than that is selected again from
+// 64-bit keys (select_row_f64), so the result is always that of the 64-bit keys.
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kRouteWarps = 4;  // rows per block
+constexpr uint32_t kFull = 0xffffffffu;
+
+// 32-bit keys against exact ones, relative to 1 + |key|: the scores' exp, log and divide
+// are good to a few units of 2^-24 and s * |z - max| (softmax) stays below 1/e; the sum
+// with the bias rounds once more. 2^-20 covers both neighbours with a factor to spare.
+constexpr float kKeyTol = 9.5367431640625e-7f;
+
+template <typename T>
+__device__ __forceinline__ float to_f32(T v);
+template <>
+__device__ __forceinline__ float to_f32<float>(float v) {
+  return v;
+}
+template <>
+__device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 v) {
+  return __bfloat162float(v);
+}
+template <>
+__device__ __forceinline__ float to_f32<__half>(__half v) {
+  return __half2float(v);
+}
+template <typename T>
+__device__ __forceinline__ T from_f32(float v);
+template <>
+__device__ __forceinline__ float from_f32<float>(float v) {
+  return v;
+}
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) {
+  return __float2bfloat16_rn(v);
+}
+template <>
+__device__ __forceinline__ __half from_f32<__half>(float v) {
+  return __float2half_rn(v);
+}
+
+// EPL consecutive elements from p (vec: p is aligned to the vector width below and all EPL exist).
+template <typename T, int EPL>
+__device__ __forceinline__ void load_run(const T* p, int n, bool vec, float (&z)[EPL]) {
+  constexpr int kBytes = EPL * static_cast<int>(sizeof(T));
+  if (vec && n >= EPL) {
+    if constexpr (kBytes % 16 == 0) {
+#pragma unroll
+      for (int q = 0; q < kBytes / 16; ++q) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + q);
+        const T* t = reinterpret_cast<const T*>(&v);
+#pragma unroll
+        for (int i = 0; i < 16 / static_cast<int>(sizeof(T)); ++i) z[q * (16 / sizeof(T)) + i] = to_f32<T>(t[i]);
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < kBytes / 8; ++q) {
+        const uint2 v = __ldg(reinterpret_cast<const uint2*>(p) + q);
+        const T* t = reinterpret_cast<const T*>(&v);
+#pragma unroll
+        for (int i = 0; i < 8 / static_cast<int>(sizeof(T)); ++i) z[q * (8 / sizeof(T)) + i] = to_f32<T>(t[i]);
+      }
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) z[i] = i < n ? to_f32<T>(p[i]) : -INFINITY;
+}
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
+  return v;
+}
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+  return v;
+}
+
+// Order-preserving map of floats to unsigned: 0 is below every float (an expert that is off).
+__device__ __forceinline__ uint32_t key_of(float v) {
+  const uint32_t b = __float_as_uint(v + 0.0f);  // -0 and +0 are equal
+  return b ^ ((b & 0x80000000u) ? 0xffffffffu : 0x80000000u);
+}
+__device__ __forceinline__ float value_of(uint32_t k) {
+  return __uint_as_float(k ^ ((k & 0x80000000u) ? 0x80000000u : 0xffffffffu));
+}
+
+__device__ __forceinline__ float sigmoid_f32(float z) {
+  const float u = expf(-fabsf(z));
+  return __fdiv_rn(z >= 0.0f ? 1.0f : u, 1.0f + u);
+}
+__device__ __forceinline__ float score_f32(float z, int score, float m, float inv_sum) {
+  if (score == kScoreSoftmax) return expf(z - m) * inv_sum;
+  if (score == kScoreSigmoid) return sigmoid_f32(z);
+  return sqrtf(fmaxf(z, 0.0f) + log1pf(expf(-fabsf(z))));
+}
+__device__ __forceinline__ double score_f64(double z, int score, double m, double sum) {
+  if (score == kScoreSoftmax) return exp(z - m) / sum;
+  if (score == kScoreSigmoid) {
+    const double u = exp(-fabs(z));
+    return (z >= 0.0 ? 1.0 : u) / (1.0 + u);
+  }
+  return sqrt(fmax(z, 0.0) + log1p(exp(-fabs(z))));
+}
+
+// Scores of selected experts up to one factor that all of a row's share (it falls out
+// of renormalised weights): with m = the largest selected logit, s_j divided by e^m
+// (softmax), e^min(m, 0) (sigmoid) or e^(min(m, 0) / 2) (sqrtsoftplus), so that no row,
+// however low its logits, divides zero by zero.
+__device__ __forceinline__ float shared_score(float z, int score, float m) {
+  if (score == kScoreSoftmax) return expf(z - m);
+  const float low = fminf(m, 0.0f);
+  if (score == kScoreSigmoid) return __fdiv_rn(expf(fminf(z, 0.0f) - low), 1.0f + expf(-fabsf(z)));
+  if (z > 0.0f) return sqrtf(z + log1pf(expf(-z)));
+  const float u = expf(z);
+  const float r = u > 0.0f ? __fdiv_rn(log1pf(u), u) : 1.0f;  // log(1 + u) / u
+  return expf(0.5f * (z - low)) * sqrtf(r);
+}
+
+struct SelectArgs {
+  int E, G, kept, k, score, sum2;
+};
+
+// The selection from 64-bit keys held in `buf` (E doubles): lane r < k gets slot r's expert or -1.
+template <typename T>
+__device__ __noinline__ int select_row_f64(const T* row, const float* bias, SelectArgs a, double* buf, int lane) {
+  double m = -INFINITY, sum = 0.0;
+  if (a.score == kScoreSoftmax) {
+    for (int e = lane; e < a.E; e += 32) m = fmax(m, static_cast<double>(to_f32<T>(row[e])));
+    for (int o = 16; o > 0; o >>= 1) m = fmax(m, __shfl_xor_sync(kFull, m, o));
+    for (int e = lane; e < a.E; e += 32) sum += exp(static_cast<double>(to_f32<T>(row[e])) - m);
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+  }
+  for (int e = lane; e < a.E; e += 32) {
+    const double z = to_f32<T>(row[e]);
+    buf[e] = z == -INFINITY ? -INFINITY
+                            : score_f64(z, a.score, m, sum) + (bias ? static_cast<double>(bias[e]) : 0.0);
+  }
+  __syncwarp();
+  const int Eg = a.E / a.G;
+  uint32_t keep = kFull;
+  if (a.kept < a.G) {
+    double w1 = -INFINITY, w2 = -INFINITY;
+    if (lane < a.G)
+      for (int j = 0; j < Eg; ++j) {
+        const double v = buf[lane * Eg + j];
+        if (v > w1) {
+          w2 = w1;
+          w1 = v;
+        } else if (v > w2) {
+          w2 = v;
+        }
+      }
+    const double worth = a.sum2 && w2 != -INFINITY ? w1 + w2 : w1;
+    int rank = 0;
+    for (int g = 0; g < a.G; ++g) {
+      const double o = __shfl_sync(kFull, worth, g);
+      rank += o > worth || (o == worth && g < lane);
+    }
+    keep = __ballot_sync(kFull, lane < a.G && rank < a.kept);
+  }
+  int mine = -1;
+  for (int r = 0; r < a.k; ++r) {
+    double bv = -INFINITY;
+    int bi = 0x7fffffff;
+    for (int e = lane; e < a.E; e += 32)
+      if (((keep >> (e / Eg)) & 1u) && buf[e] > bv) {
+        bv = buf[e];
+        bi = e;
+      }
+    for (int o = 16; o > 0; o >>= 1) {
+      const double ov = __shfl_xor_sync(kFull, bv, o);
+      const int oi = __shfl_xor_sync(kFull, bi, o);
+      if (ov > bv || (ov == bv && oi < bi)) {
+        bv = ov;
+        bi = oi;
+      }
+    }
+    if (bi == 0x7fffffff) break;  // nothing is left: the slots from r on stay empty
+    if (lane == r) mine = bi;
+    if (bi % 32 == lane) buf[bi] = -INFINITY;
+    __syncwarp();
+  }
+  return mine;
+}
+
+template <typename T, int EPL>
+__global__ void __launch_bounds__(kRouteWarps * 32)
+    route_kernel(const T* __restrict__ logits, int64_t row_stride, const float* __restrict__ bias, int rows,
+                 SelectArgs a, int renorm, float scale, int vec, int32_t* __restrict__ idx_out,
+                 float* __restrict__ w_out) {
+  extern __shared__ double key_buf[];  // E doubles per warp, where keys are sums
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int t = blockIdx.x * kRouteWarps + warp;
+  if (t >= rows) return;
+  const T* row = logits + static_cast<size_t>(t) * row_stride;
+  const int e0 = lane * EPL;
+  float z[EPL];
+  load_run<T, EPL>(row + e0, min(EPL, a.E - e0), vec != 0, z);
+
+  bool bad = false;
+  float zmax = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    bad |= !(z[i] < INFINITY);
+    zmax = fmaxf(zmax, z[i]);
+  }
+  const bool grouped = a.kept < a.G;
+  const bool need_scores = bias != nullptr || (grouped && a.sum2);
+  float inv_sum = 1.0f;
+  if (a.score == kScoreSoftmax) {
+    zmax = warp_max(zmax);
+    if (need_scores || !renorm) {
+      float s = 0.f;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) s += z[i] == -INFINITY ? 0.f : expf(z[i] - zmax);
+      inv_sum = __fdiv_rn(1.0f, warp_sum(s));
+    }
+  }
+  // keys: the scores plus bias where there is one (v), else the logits
+  uint32_t key[EPL];
+  float v[EPL];
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    const bool live = z[i] != -INFINITY;
+    v[i] = z[i];
+    if (need_scores && live) v[i] = score_f32(z[i], a.score, zmax, inv_sum);
+    if (bias != nullptr && live) {
+      v[i] += __ldg(bias + e0 + i);
+      bad |= !(fabsf(v[i]) < INFINITY);
+    }
+    key[i] = live ? key_of(bias != nullptr ? v[i] : z[i]) : 0u;
+  }
+  if (__any_sync(kFull, bad)) {
+    if (lane < a.k) {
+      idx_out[static_cast<size_t>(t) * a.k + lane] = lane;
+      w_out[static_cast<size_t>(t) * a.k + lane] = __int_as_float(0x7fc00000);
+    }
+    return;
+  }
+
+  bool unsure = false;  // two neighbours of a choice nearer than 32-bit keys tell
+  if (grouped) {
+    const int Eg = a.E / a.G;
+    float w1 = -INFINITY, w2 = -INFINITY;
+    if (Eg % EPL == 0 && ((Eg / EPL) & (Eg / EPL - 1)) == 0 && Eg / EPL <= 32) {
+      // a group is a power of two of whole lanes: merge the lanes' two largest
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        w2 = fmaxf(w2, fminf(w1, v[i]));
+        w1 = fmaxf(w1, v[i]);
+      }
+      const int lanes = Eg / EPL;
+      for (int o = 1; o < lanes; o <<= 1) {
+        const float o1 = __shfl_xor_sync(kFull, w1, o), o2 = __shfl_xor_sync(kFull, w2, o);
+        w2 = fmaxf(fmaxf(w2, o2), fminf(w1, o1));
+        w1 = fmaxf(w1, o1);
+      }
+      const int src = min(lane, a.G - 1) * lanes;  // lane g takes group g's
+      w1 = __shfl_sync(kFull, w1, src);
+      w2 = __shfl_sync(kFull, w2, src);
+    } else {
+      float* fb = reinterpret_cast<float*>(key_buf) + static_cast<size_t>(warp) * a.E;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i)
+        if (e0 + i < a.E) fb[e0 + i] = v[i];
+      __syncwarp();
+      if (lane < a.G) {
+        int j = lane % Eg;  // lanes start apart, so that a power-of-two group size does not hit one bank
+        for (int n = 0; n < Eg; ++n) {
+          const float x = fb[lane * Eg + j];
+          w2 = fmaxf(w2, fminf(w1, x));
+          w1 = fmaxf(w1, x);
+          j = j + 1 == Eg ? 0 : j + 1;
+        }
+      }
+      __syncwarp();
+    }
+    float worth = a.sum2 && w2 != -INFINITY ? w1 + w2 : w1;
+    if (lane >= a.G) worth = -INFINITY;
+    int rank = 0;
+    for (int g = 0; g < a.G; ++g) {
+      const float o = __shfl_sync(kFull, worth, g);
+      rank += o > worth || (o == worth && g < lane);
+    }
+    const bool in = lane < a.G && rank < a.kept;
+    const uint32_t keep = __ballot_sync(kFull, in);
+    if (need_scores) {
+      // the least of the kept and the best of the others
+      const float least = -warp_max(in ? -worth : -INFINITY);
+      const float best = warp_max(in ? -INFINITY : worth);
+      unsure = best != -INFINITY && least - best <= 4.0f * kKeyTol * (1.0f + fabsf(best));
+    }
+    int g = e0 / Eg, left = Eg - e0 % Eg;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      if (e0 + i < a.E && !((keep >> g) & 1u)) key[i] = 0u;
+      if (--left == 0) {
+        ++g;
+        left = Eg;
+      }
+    }
+  }
+
+  uint32_t bk = 0u;
+  int bi = 0;
+#pragma unroll
+  for (int i = 0; i < EPL; ++i)
+    if (key[i] > bk) {
+      bk = key[i];
+      bi = i;
+    }
+  int mine = -1;
+  uint32_t last = 0u;
+  for (int r = 0;; ++r) {
+    const uint32_t m = __reduce_max_sync(kFull, bk);
+    if (bias != nullptr && r > 0 && m != 0u) {
+      const float hi = value_of(last);
+      unsure |= hi - value_of(m) <= 2.0f * kKeyTol * (1.0f + fabsf(hi));
+    }
+    if (r == a.k || m == 0u) break;
+    last = m;
+    const int win = __ffs(__ballot_sync(kFull, bk == m)) - 1;
+    const int e = __shfl_sync(kFull, e0 + bi, win);
+    if (lane == r) mine = e;
+    if (lane == win) {
+      bk = 0u;
+      const int was = bi;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        if (i == was) key[i] = 0u;
+        if (key[i] > bk) {
+          bk = key[i];
+          bi = i;
+        }
+      }
+    }
+  }
+  if (unsure) mine = select_row_f64<T>(row, bias, a, key_buf + static_cast<size_t>(warp) * a.E, lane);
+
+  const bool has = mine >= 0;
+  const float zs = has ? to_f32<T>(row[mine]) : -INFINITY;
+  float w = 0.f;
+  if (renorm) {
+    const float m = warp_max(zs);
+    const float s = has ? shared_score(zs, a.score, m) : 0.f;
+    const float sum = warp_sum(s);
+    if (has) w = scale * __fdiv_rn(s, sum);
+  } else if (has) {
+    w = scale * score_f32(zs, a.score, zmax, inv_sum);
+  }
+  if (lane < a.k) {
+    idx_out[static_cast<size_t>(t) * a.k + lane] = mine;
+    w_out[static_cast<size_t>(t) * a.k + lane] = w;
+  }
+}
+
+// Gradient of the logits from the weights' gradients g, the selection held fixed. With
+// p_j = s_j / S the renormalised scores and gbar = sum_j g_j p_j:
+//   renormalised: softmax       dz_j = scale p_j (g_j - gbar)
+//                 sigmoid       dz_j = scale p_j (g_j - gbar) (1 - s_j)
+//                 sqrtsoftplus  dz_j = scale p_j (g_j - gbar) sigmoid(z_j) / (2 softplus(z_j))
+//   otherwise:    sigmoid, sqrtsoftplus: s_j in the place of p_j and gbar = 0
+//                 softmax       dz_e = s_e (scale g_e [e selected] - scale sum_j g_j s_j), every e
+// One warp per row; lane r holds slot r. The row is written once, 16 bytes a lane, each
+// vector gathering the slots that fall into it (an expert named twice adds up).
+template <typename T>
+__global__ void __launch_bounds__(kRouteWarps * 32)
+    route_grad_kernel(const float* __restrict__ grad_w, const T* __restrict__ logits, int64_t row_stride,
+                      const int32_t* __restrict__ idx, int rows, int E, int k, int score, int renorm, float scale,
+                      int vec_in, int vec_out, T* __restrict__ out) {
+  constexpr int V = 16 / static_cast<int>(sizeof(T));
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int t = blockIdx.x * kRouteWarps + warp;
+  if (t >= rows) return;
+  const T* row = logits + static_cast<size_t>(t) * row_stride;
+  int e = lane < k ? __ldg(idx + static_cast<size_t>(t) * k + lane) : -1;
+  if (e >= E) e = -1;  // not an expert: no gradient, and no read outside the row
+  const bool has = e >= 0;
+  const float g = has ? __ldg(grad_w + static_cast<size_t>(t) * k + lane) : 0.f;
+  const float zs = has ? to_f32<T>(row[e]) : -INFINITY;
+  const bool dense = score == kScoreSoftmax && !renorm;
+  float zmax = -INFINITY, inv_sum = 0.f, back = 0.f;
+  float d = 0.f;  // the slot's own term
+  if (dense) {
+    float s = 0.f;
+    for (int c = lane * V; c < E; c += 32 * V) {
+      float z[V];
+      load_run<T, V>(row + c, min(V, E - c), vec_in != 0, z);
+      // running maximum and sum: one pass over the row
+      float m = zmax;
+#pragma unroll
+      for (int i = 0; i < V; ++i) m = fmaxf(m, z[i]);
+      if (m != -INFINITY) {
+        s *= expf(zmax - m);
+#pragma unroll
+        for (int i = 0; i < V; ++i) s += expf(z[i] - m);
+        zmax = m;
+      }
+    }
+    const float m = warp_max(zmax);
+    s = m == -INFINITY ? 0.f : warp_sum(s * expf(zmax - m));
+    zmax = m;
+    inv_sum = s > 0.f || s != s ? __fdiv_rn(1.0f, s) : 0.f;
+    const float sj = has && zs != -INFINITY ? expf(zs - zmax) * inv_sum : 0.f;
+    d = scale * g;
+    back = warp_sum(d * sj);
+  } else {
+    float p, gbar = 0.f;
+    if (renorm) {
+      const float m = warp_max(zs);
+      p = has && zs != -INFINITY ? shared_score(zs, score, m) : 0.f;
+      const float sum = warp_sum(p);
+      p = sum > 0.f || sum != sum ? __fdiv_rn(p, sum) : 0.f;
+      gbar = warp_sum(g * p);
+    } else {
+      p = has ? score_f32(zs, score, 0.f, 1.f) : 0.f;
+    }
+    float slope = 1.0f;
+    if (score == kScoreSigmoid) {
+      slope = sigmoid_f32(-zs);
+    } else if (score == kScoreSqrtSoftplus) {
+      const float u = expf(-fabsf(zs));
+      // sigmoid / softplus; for z <= 0 both over e^z, so that it tends to 1
+      slope = zs > 0.f ? __fdiv_rn(1.0f, (1.0f + u) * (zs + log1pf(u)))
+                       : __fdiv_rn(1.0f, (1.0f + u) * (u > 0.f ? __fdiv_rn(log1pf(u), u) : 1.0f));
+      slope *= 0.5f;
+    }
+    d = has ? scale * p * (g - gbar) * slope : 0.f;
+  }
+  T* orow = out + static_cast<size_t>(t) * E;
+  for (int c0 = 0; c0 < E; c0 += 32 * V) {
+    const int c = c0 + lane * V;
+    float acc[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] = 0.f;
+    for (int r = 0; r < k; ++r) {
+      const int er = __shfl_sync(kFull, e, r);
+      const float dr = __shfl_sync(kFull, d, r);
+      if (er >= 0) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] += er == c + i ? dr : 0.f;
+      }
+    }
+    if (dense && c < E) {
+      float z[V];
+      load_run<T, V>(row + c, min(V, E - c), vec_in != 0, z);
+#pragma unroll
+      for (int i = 0; i < V; ++i) acc[i] = z[i] == -INFINITY ? 0.f : expf(z[i] - zmax) * inv_sum * (acc[i] - back);
+    }
+    if (vec_out && c + V <= E) {
+      uint4 o;
+      T* ot = reinterpret_cast<T*>(&o);
+#pragma unroll
+      for (int i = 0; i < V; ++i) ot[i] = from_f32<T>(acc[i]);
+      *reinterpret_cast<uint4*>(orow + c) = o;
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (c + i < E) orow[c + i] = from_f32<T>(acc[i]);
+    }
+  }
+}
+
+template <typename T, int EPL>
+cudaError_t launch_route_epl(const RouteArgs& r, cudaStream_t s) {
+  constexpr int kBytes = EPL * static_cast<int>(sizeof(T));
+  const uintptr_t vb = kBytes % 16 == 0 ? 16 : 8;
+  const bool vec = reinterpret_cast<uintptr_t>(r.logits) % vb == 0 && (r.row_stride * sizeof(T)) % vb == 0;
+  const bool grouped = r.topk_groups < r.n_groups;
+  // 64-bit keys of the rows that need them, and the groups' keys where lanes do not align with groups
+  const bool need = grouped || r.bias != nullptr;
+  const size_t smem = need ? static_cast<size_t>(kRouteWarps) * r.E * sizeof(double) : 0;
+  const SelectArgs a{r.E, r.n_groups, r.topk_groups, r.k, r.score, r.group_sum2};
+  route_kernel<T, EPL><<<(r.T + kRouteWarps - 1) / kRouteWarps, kRouteWarps * 32, smem, s>>>(
+      static_cast<const T*>(r.logits), r.row_stride, r.bias, r.T, a, r.renorm, r.scale, vec ? 1 : 0, r.idx, r.w);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_route_t(const RouteArgs& r, cudaStream_t s) {
+  if (r.E <= 128) return launch_route_epl<T, 4>(r, s);
+  if (r.E <= 256) return launch_route_epl<T, 8>(r, s);
+  if (r.E <= 384) return launch_route_epl<T, 12>(r, s);
+  return launch_route_epl<T, 16>(r, s);
+}
+
+template <typename T>
+cudaError_t launch_route_grad_t(const RouteGradArgs& r, cudaStream_t s) {
+  const bool vi = reinterpret_cast<uintptr_t>(r.logits) % 16 == 0 && (r.row_stride * sizeof(T)) % 16 == 0;
+  const bool vo = reinterpret_cast<uintptr_t>(r.out) % 16 == 0 && (r.E * sizeof(T)) % 16 == 0;
+  route_grad_kernel<T><<<(r.T + kRouteWarps - 1) / kRouteWarps, kRouteWarps * 32, 0, s>>>(
+      r.grad_w, static_cast<const T*>(r.logits), r.row_stride, r.idx, r.T, r.E, r.k, r.score, r.renorm, r.scale,
+      vi ? 1 : 0, vo ? 1 : 0, static_cast<T*>(r.out));
+  return cudaGetLastError();
+}
+
+// A caller's routing into the layer's own buffers. -1 is an empty slot; any other index
+// outside [0, E) gets the slot's placeholder expert with a NaN weight and is reported.
+__global__ void __launch_bounds__(256)
+    take_routing_kernel(const int32_t* __restrict__ idx_in, const float* __restrict__ w_in, int n, int k, int E,
+                        int32_t* __restrict__ idx, float* __restrict__ w, int* status) {
+  const int i = blockIdx.x * blockDim.x + threadIdx.x;
+  if (i >= n) return;
+  int e = idx_in[i];
+  float wi = w_in[i];
+  if (e < -1 || e >= E) {
+    report_status(status, kStatusDevice);
+    e = i % k;
+    wi = __int_as_float(0x7fc00000);
+  }
+  idx[i] = e;
+  w[i] = wi;
+}
+
+}  // namespace
+
+cudaError_t launch_route(const RouteArgs& r, cudaStream_t s) {
+  if (r.T == 0) return cudaSuccess;
+  if (r.E > 512 || r.k > 32 || r.n_groups > 32) return cudaErrorInvalidValue;
+  if (r.dtype == kValFp32) return launch_route_t<float>(r, s);
+  if (r.dtype == kValBf16) return launch_route_t<__nv_bfloat16>(r, s);
+  return launch_route_t<__half>(r, s);
+}
+
+cudaError_t launch_route_grad(const RouteGradArgs& r, cudaStream_t s) {
+  if (r.T == 0) return cudaSuccess;
+  if (r.k > 32) return cudaErrorInvalidValue;
+  if (r.dtype == kValFp32) return launch_route_grad_t<float>(r, s);
+  if (r.dtype == kValBf16) return launch_route_grad_t<__nv_bfloat16>(r, s);
+  return launch_route_grad_t<__half>(r, s);
+}
+
+cudaError_t launch_take_routing(const int32_t* idx_in, const float* w_in, int T, int k, int E, int32_t* idx, float* w,
+                                int* status, cudaStream_t s) {
+  const int n = T * k;
+  take_routing_kernel<<<(n + 255) / 256, 256, 0, s>>>(idx_in, w_in, n, k, E, idx, w, status);
+  return cudaGetLastError();
+}
+
+}  // namespace moe

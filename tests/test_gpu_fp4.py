@@ -1,0 +1,299 @@
+"""Microscaled FP4 quantisation and products against plain float64 forms.
+
+Quantisation is compared bit for bit: the rule decides every code exactly. Products: E2M1 x E2M1 with scales are
+exact in the MMA up to its fp32 accumulation, K / 64 steps of at most two units of 2^-24 (it may truncate) of the
+running sum, which stays below sum |x w|; then one rounding of the result to its type.
+"""
+import numpy as np
+import pytest
+import torch
+
+import routed_expert_ffn_sqrtsoftplus_b200 as moe
+from routed_expert_ffn_sqrtsoftplus_b200 import build
+
+import fp4_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+DT = {"fp32": torch.float32, "bf16": torch.bfloat16, "fp16": torch.float16}
+FMT = ["mxfp4", "nvfp4"]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built(cuda_device):
+    build.build()
+
+
+def _gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def _x(rows, K, dtype, seed):
+    g = _gen(seed)
+    x = torch.randn((rows, K), generator=g) * torch.exp(torch.randn((1, K), generator=g))
+    if rows > 2:
+        x[1] = 0.0
+        x[2, :16] = 0.0
+    return x.to(DT[dtype])
+
+
+def _ts(x, fmt):
+    return (x.abs().max().float() / 2688.0).reshape(1) if fmt == "nvfp4" else None
+
+
+def _check_quant(x, fmt, ts=None):
+    codes, scales = moe.quantize_fp4(x.cuda(), fmt, None if ts is None else ts.cuda())
+    rc, rs, rv = ref.quantize(x.double().numpy(), fmt, None if ts is None else ts.item())
+    assert np.array_equal(scales.cpu().numpy(), rs)
+    diff = codes.cpu().numpy() != rc
+    assert not diff.any(), (np.argwhere(diff)[:4], diff.sum())
+    return codes, scales, rv
+
+
+@pytest.mark.parametrize("fmt", FMT)
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("rows,K", [(1, 32), (3, 64), (33, 96), (7, 2304), (130, 416)])
+def test_quantize(fmt, dtype, rows, K):
+    x = _x(rows, K, dtype, rows + K)
+    for ts in ((None, _ts(x, fmt)) if fmt == "nvfp4" else (None,)):
+        codes, scales, rv = _check_quant(x, fmt, ts)
+        for out in DT.values():
+            v = moe.dequantize_fp4(codes, scales, fmt, None if ts is None else ts.cuda(), dtype=out)
+            want = torch.from_numpy(rv).float()           # e2m1 * d, one rounding to 32 bits
+            # two roundings at most (32 bits, then the type); fp16 may be subnormal
+            err = (v.cpu().double() - torch.from_numpy(rv)).abs()
+            tiny = torch.finfo(out).smallest_normal * torch.finfo(out).eps
+            top = torch.finfo(out).max
+            ok = err <= want.abs().double() * (torch.finfo(out).eps / 2 + 2.0 ** -24) + tiny
+            assert bool((ok | (want.abs() > top)).all())
+
+
+@pytest.mark.parametrize("fmt", FMT)
+def test_quantize_borders(fmt):
+    """Values on, and one step beside, every border of both grids."""
+    rows = []
+    for unit in (1.0, 0.75, 1.125, 2.0 ** -5, 208.0, 3.0 * 2.0 ** -7):
+        b = []
+        for e in (0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 0.5, 1.0, 3.0):
+            v = np.float32(e * unit)
+            b += [v, np.nextafter(v, np.float32(0)), np.nextafter(v, np.float32(1e9)), -v]
+        b = b[:30] + [6.0 * unit, 0.0]
+        rows.append(b)
+        b = list(b)
+        rows.append([6.0 * unit if i % 16 == 0 else v for i, v in enumerate(b)])
+    x = torch.tensor(np.array(rows, dtype=np.float32))
+    _check_quant(x, fmt)
+    if fmt == "nvfp4":
+        for t in (0.3, 1.0 / 3.0, 7e-4):
+            ts = torch.tensor([t], dtype=torch.float32)
+            _check_quant(x, fmt, ts)
+            _check_quant((x * ts).float(), fmt, ts)
+        # block maxima at and beside the borders of the scale's grid
+        mids = (ref.E4M3[1:] + ref.E4M3[:-1]) / 2 * 6
+        y = torch.zeros((len(mids) * 3, 32))
+        for i, m in enumerate(mids.astype(np.float32)):
+            for j, v in enumerate((m, np.nextafter(m, np.float32(0)), np.nextafter(m, np.float32(1e9)))):
+                y[3 * i + j, 3] = float(v)
+                y[3 * i + j, 20] = -float(v) / 3
+        _check_quant(y, fmt)
+        _check_quant(y, fmt, torch.tensor([0.3]))
+
+
+@pytest.mark.parametrize("fmt", FMT)
+def test_quantize_matches_the_weight_quantiser_and_strides(fmt):
+    x = _x(9, 128, "bf16", 4).cuda()
+    if fmt == "mxfp4":
+        c0, s0 = moe.quantize_mxfp4(x)
+        c1, s1 = moe.quantize_fp4(x, fmt)
+        assert torch.equal(c0, c1) and torch.equal(s0, s1)
+    wide = torch.randn((9, 131), generator=_gen(3)).cuda()
+    for dtype in DT.values():
+        v = wide.to(dtype)[:, 1:129]
+        a, b = moe.quantize_fp4(v, fmt), moe.quantize_fp4(v.contiguous(), fmt)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    c, s = moe.quantize_fp4(torch.empty((0, 64), device="cuda"), fmt)
+    assert c.shape == (0, 32) and moe.dequantize_fp4(c, s, fmt).shape == (0, 64)
+
+
+@pytest.mark.parametrize("fmt", FMT)
+def test_quantize_not_finite_and_extreme(fmt):
+    x = torch.randn((3, 96), generator=_gen(8))
+    x[0, 5] = float("nan")
+    x[1, 40] = -float("inf")
+    codes, scales = moe.quantize_fp4(x.cuda(), fmt)
+    v = moe.dequantize_fp4(codes, scales, fmt, dtype=torch.float32).cpu()
+    bs = ref.BLOCK[fmt]
+    bad = torch.zeros((3, 96 // bs), dtype=torch.bool)
+    bad[0, 5 // bs] = bad[1, 40 // bs] = True
+    assert torch.equal(torch.isnan(v).view(3, -1, bs).all(2), bad) and torch.equal(torch.isnan(v).view(3, -1, bs).any(2), bad)
+    big = torch.full((2, 64), torch.finfo(torch.float32).max)
+    big[1] = torch.finfo(torch.float32).smallest_normal / 8
+    _check_quant(big, fmt)
+
+
+# ------------------------------------------------------------------ products
+def _weights(E, N, K, fmt, seed):
+    w = torch.randn((E * N, K), generator=_gen(seed)) / K ** 0.5
+    ts = None
+    if fmt == "nvfp4":
+        ts = torch.linspace(0.5, 2.0, E).float()
+    codes, scales, _ = ref.quantize(w.double().numpy(), fmt)
+    return (torch.from_numpy(codes).view(E, N, K // 2).cuda(), torch.from_numpy(scales).view(E, N, -1).cuda(),
+            None if ts is None else ts.cuda())
+
+
+def _bound(xv, wv, want, out):
+    K = xv.shape[1]
+    mag = np.abs(xv) @ np.abs(wv).T
+    eps = torch.finfo(out).eps / 2
+    return mag * (K / 64 + 4) * 2 * 2.0 ** -24 + np.abs(want) * eps * 1.01 + (2.0 ** -25 if out == torch.float16 else 0)
+
+
+def _check_matmul(T, N, K, fmt, out=torch.bfloat16, seed=0):
+    x = _x(T, K, "bf16", seed + 1)
+    xts = _ts(x, fmt)
+    xc, xs, _ = ref.quantize(x.double().numpy(), fmt, None if xts is None else xts.item())
+    w, ws, wts = _weights(1, N, K, fmt, seed + 2)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kw = dict(x_tensor_scale=None if xts is None else xts.cuda(), w_tensor_scale=wts)
+    y = moe.fp4_matmul(torch.from_numpy(xc).cuda(), torch.from_numpy(xs).cuda(), w[0], ws[0], fmt, out_dtype=out,
+                       status=status, **kw)
+    xv = ref.values(xc, xs, fmt, None if xts is None else xts.numpy())
+    wv = ref.values(w[0].cpu().numpy(), ws[0].cpu().numpy(), fmt, None if wts is None else wts.cpu().numpy()[0])
+    want = xv @ wv.T
+    assert status.item() == 0
+    err = np.abs(y.double().cpu().numpy() - want)
+    b = _bound(xv, wv, want, out)
+    assert (err <= b).all(), (np.argwhere(err > b)[:5], (err / np.maximum(b, 1e-300)).max())
+    z = moe.fp4_linear(x.cuda(), w[0], ws[0], fmt, out=torch.empty_like(y), **kw)
+    assert torch.equal(y, z)
+
+
+@pytest.mark.parametrize("fmt", FMT)
+@pytest.mark.parametrize("T,N,K", [(1, 1, 32), (1, 128, 256), (16, 128, 512), (3, 200, 96), (17, 130, 288), (32, 384, 1024),
+                                   (5, 4608, 5120), (1, 640, 2304)])
+def test_matmul_few_tokens(fmt, T, N, K):
+    _check_matmul(T, N, K, fmt)
+
+
+@pytest.mark.parametrize("fmt", FMT)
+@pytest.mark.parametrize("T,N,K", [(33, 256, 256), (64, 100, 320), (96, 1000, 1312), (97, 256, 512), (192, 512, 768),
+                                   (193, 300, 800), (500, 700, 2080), (1024, 2304, 512)])
+def test_matmul_many_tokens(fmt, T, N, K):
+    _check_matmul(T, N, K, fmt)
+
+
+@pytest.mark.parametrize("fmt", FMT)
+@pytest.mark.parametrize("out", [torch.float32, torch.float16])
+def test_matmul_output_types(fmt, out):
+    for T in (7, 70, 210):
+        _check_matmul(T, 333, 544, fmt, out)
+
+
+@pytest.mark.parametrize("fmt", FMT)
+@pytest.mark.parametrize("E,N,K,sizes,pad", [
+    (4, 128, 256, [3, 0, 40, 1], 0), (1, 64, 64, [5], 3), (7, 300, 512, [0, 0, 1, 0, 200, 33, 0], 9),
+    (64, 130, 288, [i % 5 for i in range(64)], 2), (40, 256, 320, [(7 * i) % 11 * 9 for i in range(40)], 0),
+    (3, 512, 256, [0, 0, 0], 4), (512, 32, 64, [1 if i % 3 else 0 for i in range(512)], 1)])
+def test_experts(fmt, E, N, K, sizes, pad):
+    T = sum(sizes) + pad
+    x = _x(T, K, "bf16", E + N)
+    xts = _ts(x, fmt)
+    w, ws, wts = _weights(E, N, K, fmt, E)
+    off = torch.tensor([0] + list(np.cumsum(sizes)), dtype=torch.int32).cuda()
+    y = torch.full((T, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    moe.fp4_linear(x.cuda(), w, ws, fmt, x_tensor_scale=None if xts is None else xts.cuda(), w_tensor_scale=wts,
+                   offsets=off, out=y)
+    _, _, xv = ref.quantize(x.double().numpy(), fmt, None if xts is None else xts.item())
+    got = y.double().cpu().numpy()
+    assert (got[T - pad:] == 7.0).all()          # rows behind the last expert's stay as they were
+    for g in range(E):
+        a, b = int(off[g]), int(off[g + 1])
+        if a == b:
+            continue
+        wv = ref.values(w[g].cpu().numpy(), ws[g].cpu().numpy(), fmt, None if wts is None else wts.cpu().numpy()[g])
+        want = xv[a:b] @ wv.T
+        assert (np.abs(got[a:b] - want) <= _bound(xv[a:b], wv, want, torch.bfloat16)).all(), g
+
+
+def test_experts_offsets_are_clamped():
+    """Offsets out of range or out of order lead nowhere outside x and y: such experts have fewer rows, or none."""
+    E, N, K, T = 4, 64, 64, 50
+    x = _x(T, K, "bf16", 1).cuda()
+    w, ws, _ = _weights(E, N, K, "mxfp4", 2)
+    for bad, good in (([0, 20, 10, 30, 50], [0, 20, 20, 30, 50]), ([-5, 7, 9, 1000, 2000], [0, 7, 9, 50, 50]),
+                      ([10, 20, 30, 40, 45], [10, 20, 30, 40, 45])):
+        ya, yb = (torch.full((T, N), 3.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        moe.fp4_linear(x, w, ws, "mxfp4", offsets=torch.tensor(bad, dtype=torch.int32).cuda(), out=ya)
+        moe.fp4_linear(x, w, ws, "mxfp4", offsets=torch.tensor(good, dtype=torch.int32).cuda(), out=yb)
+        assert torch.equal(ya, yb)
+        assert bool((ya[:good[0]] == 3.0).all()) and bool((ya[good[-1]:] == 3.0).all())
+
+
+@pytest.mark.parametrize("fmt", FMT)
+def test_matmul_nan_stays_in_its_row(fmt):
+    x = _x(40, 96, "bf16", 2)
+    x[7, 3] = float("nan")
+    x[33] = float("inf")
+    w, ws, wts = _weights(1, 150, 96, fmt, 3)
+    y = moe.fp4_linear(x.cuda(), w[0], ws[0], fmt)
+    bad = torch.isnan(y).all(1)
+    assert bad.nonzero().flatten().tolist() == [7, 33] and not bool(torch.isnan(y[~bad]).any())
+
+
+def test_strided_x_streams_and_graphs():
+    x = torch.randn((300, 416), generator=_gen(4)).to(torch.bfloat16).cuda()
+    w, ws, wts = _weights(1, 256, 384, "nvfp4", 5)
+    ts = torch.tensor([0.01]).cuda()
+    for T in (8, 300):
+        v = x[:T, 8:392]
+        y0 = moe.fp4_linear(v.contiguous(), w[0], ws[0], "nvfp4", x_tensor_scale=ts, w_tensor_scale=wts)
+        assert torch.equal(y0, moe.fp4_linear(v, w[0], ws[0], "nvfp4", x_tensor_scale=ts, w_tensor_scale=wts))
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        ys = [moe.fp4_linear(v, w[0], ws[0], "nvfp4", x_tensor_scale=ts, w_tensor_scale=wts, stream=s) for _ in range(8)]
+        s.synchronize()
+        assert all(torch.equal(y0, y) for y in ys)
+        src = v.clone()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            yg = moe.fp4_linear(src, w[0], ws[0], "nvfp4", x_tensor_scale=ts, w_tensor_scale=wts)
+        src.copy_(x[:T, :384])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(yg, moe.fp4_linear(x[:T, :384], w[0], ws[0], "nvfp4", x_tensor_scale=ts, w_tensor_scale=wts))
+
+
+def test_route_then_experts():
+    """A 4-bit expert layer from the operators: route, sort by expert, gate and up, SwiGLU, down, weighted sum."""
+    T, E, H, I, k = 37, 8, 256, 128, 2
+    g = _gen(11)
+    x = torch.randn((T, H), generator=g).to(torch.bfloat16).cuda()
+    wg = (torch.randn((E, H), generator=g) / H ** 0.5).cuda()
+    w13, s13, _ = _weights(E, 2 * I, H, "mxfp4", 12)
+    w2, s2, _ = _weights(E, H, I, "mxfp4", 13)
+    idx, w = moe.route(x.float() @ wg.t(), k, score="sigmoid", n_groups=2, topk_groups=1)
+    flat = idx.flatten().long()
+    order = torch.argsort(flat, stable=True)
+    off = torch.cat([flat.new_zeros(1), torch.bincount(flat, minlength=E).cumsum(0)]).to(torch.int32)
+    gu = moe.fp4_linear(x[order // k], w13, s13, "mxfp4", offsets=off).float()
+    h = (torch.nn.functional.silu(gu[:, :I]) * gu[:, I:]).to(torch.bfloat16)
+    o = moe.fp4_linear(h, w2, s2, "mxfp4", offsets=off, out=torch.empty((T * k, H), device="cuda"))
+    y = torch.zeros((T, H), device="cuda").index_add_(0, order // k, o * w.flatten()[order][:, None])
+    hn = h.double().cpu().numpy()
+    _, _, xv = ref.quantize(x.double().cpu().numpy(), "mxfp4")
+    _, _, hv = ref.quantize(hn, "mxfp4")
+    want = np.zeros((T, H))
+    mag = np.zeros((T, H))
+    for r, s in enumerate(order.tolist()):
+        e, t = int(flat[s]), s // k
+        wv = ref.values(w13[e].cpu().numpy(), s13[e].cpu().numpy(), "mxfp4")
+        gv = wv @ xv[t]
+        a, b = gv[:I], gv[I:]
+        ref_h = a / (1 + np.exp(-a)) * b
+        # gate and up are rounded to BF16 (2^-9 each, SiLU's slope at most 1.1), and the product once more
+        assert (np.abs(hn[r] - ref_h) <= 2.0 ** -7 * np.abs(b) * (np.abs(a) + 0.3) + 1e-6).all()
+        dv = ref.values(w2[e].cpu().numpy(), s2[e].cpu().numpy(), "mxfp4")
+        want[t] += float(w.flatten()[s]) * (dv @ hv[r])
+        mag[t] += float(w.flatten()[s]) * (np.abs(dv) @ np.abs(hv[r]))
+    assert (np.abs(y.double().cpu().numpy() - want) <= mag * 16 * 2.0 ** -24).all()

@@ -1,0 +1,144 @@
+"""Refusals of the handle-less operators, before any GPU is touched, and the reference forms of their tests."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import routed_expert_ffn_sqrtsoftplus_b200 as moe
+from routed_expert_ffn_sqrtsoftplus_b200 import build as moe_build
+
+import fp4_ref as ref
+
+FAKE = 0x10000  # 16-byte aligned, never dereferenced: each call is refused first
+INV, UNS, OK = moe.MOE_ERR_INVALID_ARG, moe.MOE_ERR_UNSUPPORTED, moe.MOE_OK
+
+
+@pytest.fixture(scope="module")
+def L():
+    moe_build.build()
+    return moe.lib()
+
+
+def _cfg(**kw):
+    d = dict(n_experts=64, top_k=4, n_groups=4, topk_groups=2, score=1, group_top2=1, renormalize=1, route_scale=1.0)
+    d.update(kw)
+    return moe._RouteConfig(*[d[n] for n, _ in moe._RouteConfig._fields_])
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(n_experts=0), INV), (dict(top_k=0), INV), (dict(n_groups=0), INV), (dict(topk_groups=0), INV),
+    (dict(topk_groups=5), INV), (dict(n_experts=63), INV), (dict(top_k=33, topk_groups=2), INV),
+    (dict(score=3), INV), (dict(score=-1), INV), (dict(route_scale=0.0), INV), (dict(route_scale=float("nan")), INV),
+    (dict(route_scale=float("inf")), INV), (dict(n_experts=516), UNS), (dict(top_k=33, topk_groups=4), UNS),
+    (dict(n_experts=66, n_groups=33, topk_groups=33), UNS)])
+def test_route_refuses_bad_configs(L, kw, want):
+    assert L.moe_route(_cfg(**kw), FAKE, 2, 1024, None, 3, FAKE, FAKE, None) == want
+    assert L.moe_route_backward(_cfg(**kw), FAKE, FAKE, 2, 1024, FAKE, 3, FAKE, None) == want
+
+
+def test_route_refuses_bad_arguments(L):
+    c = _cfg()
+    assert L.moe_route(None, FAKE, 2, 64, None, 3, FAKE, FAKE, None) == INV
+    assert L.moe_route(c, None, 2, 64, None, 3, FAKE, FAKE, None) == INV
+    assert L.moe_route(c, FAKE, 3, 64, None, 3, FAKE, FAKE, None) == INV
+    assert L.moe_route(c, FAKE, 2, 63, None, 3, FAKE, FAKE, None) == INV
+    assert L.moe_route(c, FAKE, 2, 64, None, -1, FAKE, FAKE, None) == INV
+    assert L.moe_route(c, FAKE + 2, 2, 64, None, 3, FAKE, FAKE, None) == INV
+    assert L.moe_route(c, FAKE, 2, 64, FAKE + 1, 3, FAKE, FAKE, None) == INV
+    assert L.moe_route(c, FAKE, 2, 64, None, 3, None, FAKE, None) == INV
+    assert L.moe_route(c, None, 2, 64, None, 0, None, None, None) == OK
+    assert L.moe_route_backward(c, FAKE, FAKE, 2, 64, FAKE, 3, FAKE, None) == INV    # in place
+    assert L.moe_route_backward(c, None, FAKE, 2, 64, FAKE, 3, FAKE + 64, None) == INV
+    assert L.moe_route_backward(c, None, None, 2, 64, None, 0, None, None) == OK
+    assert L.moe_forward_routed(None, FAKE, FAKE, FAKE, 1, FAKE, None) == INV
+
+
+def test_fp4_refuses_bad_arguments(L):
+    q, d = L.moe_quantize_fp4, L.moe_dequantize_fp4
+    assert q(2, FAKE, 0, 4, 64, 64, None, FAKE, FAKE, 4, None) == INV
+    assert q(0, FAKE, 5, 4, 64, 64, None, FAKE, FAKE, 4, None) == INV
+    assert q(0, FAKE, 0, 4, 48, 48, None, FAKE, FAKE, 4, None) == INV
+    assert q(0, FAKE, 0, 4, 64, 63, None, FAKE, FAKE, 4, None) == INV
+    assert q(0, FAKE, 0, 4, 64, 64, None, FAKE, FAKE, 1, None) == INV
+    assert q(1, FAKE, 0, 4, 64, 64, None, FAKE, FAKE, 3, None) == INV
+    assert q(0, FAKE, 0, 4, 64, 64, FAKE, FAKE, FAKE, 4, None) == INV     # MXFP4 has no tensor scale
+    assert q(0, FAKE + 1, 0, 4, 64, 64, None, FAKE, FAKE, 4, None) == INV
+    assert q(0, FAKE, 0, 4, 64, 64, None, FAKE + 8, FAKE, 4, None) == INV
+    assert q(0, None, 0, 4, 64, 64, None, FAKE, FAKE, 4, None) == INV
+    assert q(0, FAKE, 0, -1, 64, 64, None, FAKE, FAKE, 4, None) == INV
+    assert q(0, FAKE, 0, 1 << 40, 64, 64, None, FAKE, FAKE, 4, None) == UNS
+    assert q(0, None, 0, 0, 64, 64, None, None, None, 4, None) == OK
+    assert d(0, FAKE, FAKE, 4, 64, 1, None, FAKE, 0, None) == INV
+    assert d(1, FAKE, FAKE, 4, 40, 4, None, FAKE, 0, None) == INV
+    assert d(0, FAKE, FAKE, 4, 64, 2, FAKE, FAKE, 0, None) == INV
+    assert d(0, None, None, 0, 64, 2, None, None, 0, None) == OK
+
+
+def _product(**kw):
+    d = dict(format=0, T=4, N=64, K=64, E=1, out_dtype=0, x=FAKE, x_scales=FAKE, x_scale_stride=2, x_tensor_scale=None,
+             w=FAKE, w_scales=FAKE, w_scale_stride=2, w_tensor_scale=None, offsets=None, y=FAKE, status=None)
+    d.update(kw)
+    return moe._Fp4Product(*[d[n] for n, _ in moe._Fp4Product._fields_])
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(format=2), INV), (dict(T=-1), INV), (dict(N=0), INV), (dict(K=48), INV), (dict(K=0), INV), (dict(E=0), INV),
+    (dict(E=2), INV), (dict(out_dtype=3), INV), (dict(x_scale_stride=1), INV), (dict(format=1), INV),
+    (dict(x_tensor_scale=FAKE), INV), (dict(w_tensor_scale=FAKE), INV), (dict(x=None), INV), (dict(w=FAKE + 8), INV),
+    (dict(x=FAKE + 4), INV), (dict(y=FAKE + 1), INV), (dict(y=None), INV), (dict(w_scales=None), INV),
+    (dict(offsets=FAKE + 2), INV), (dict(T=(1 << 22) + 1), UNS), (dict(E=513, offsets=FAKE), UNS),
+    (dict(N=(1 << 18) + 1), UNS), (dict(T=0, x=None, y=None), OK)])
+def test_fp4_matmul_refuses_bad_arguments(L, kw, want):
+    assert L.moe_fp4_matmul(_product(**kw), None) == want
+    assert L.moe_fp4_matmul(None, None) == INV
+
+
+def test_bindings_refuse_bad_tensors(L):
+    z = torch.zeros((4, 8))
+    for call in (lambda: moe.route(z, 2), lambda: moe.route_backward(z, z, z), lambda: moe.quantize_fp4(z, "mxfp4"),
+                 lambda: moe.quantize_fp4(z, "fp5"), lambda: moe.dequantize_fp4(z, z, "mxfp4"),
+                 lambda: moe.fp4_linear(z, z, z, "mxfp4"), lambda: moe.fp4_matmul(z, z, z, z, "nvfp4"),
+                 lambda: moe.fp4_matmul(z, z, z, z, "e2m1")):
+        with pytest.raises(ValueError):
+            call()
+
+
+# ------------------------------------------------------------------ the references themselves
+def test_reference_grid_and_codes():
+    assert ref.E4M3[126] == 448 and ref.E4M3[1] == 2.0 ** -9 and ref.E4M3[8] == 2.0 ** -6
+    t = torch.arange(127, dtype=torch.uint8).view(torch.float8_e4m3fn).double().numpy()
+    assert np.array_equal(t, ref.E4M3)
+    # every half-way point goes to the even code
+    for i in range(7):
+        mid = (ref.GRID[i] + ref.GRID[i + 1]) / 2
+        assert ref.nearest(np.array([mid]), ref.GRID)[0] % 2 == 0
+        x = np.zeros((1, 32))
+        x[0, 0], x[0, 1] = 6.0, mid
+        c, s, v = ref.quantize(x, "mxfp4")
+        assert s[0, 0] == 127 and (c[0, 0] >> 4) == ref.nearest(np.array([mid]), ref.GRID)[0]
+        assert np.array_equal(ref.values(c, s, "mxfp4"), v)
+
+
+def test_reference_routing_by_hand():
+    z = np.log(np.array([[1.0, 2.0, 3.0, 4.0]]))
+    idx, w = ref.route(z, 2, "softmax", renorm=False)
+    assert idx.tolist() == [[3, 2]] and np.allclose(w, [[0.4, 0.3]])
+    idx, w = ref.route(z, 2, "softmax", bias=np.array([1.0, 0, 0, 0]))
+    assert idx.tolist() == [[0, 3]] and np.allclose(w, [[0.2, 0.8]])
+    # groups {0, 1} and {2, 3}: 0.1 + 1 + 0.2 against 0.7
+    idx, w = ref.route(z, 2, "softmax", bias=np.array([1.0, 0, 0, 0]), G=2, kept=1)
+    assert idx.tolist() == [[0, 1]] and np.allclose(w, [[1 / 3, 2 / 3]])
+    idx, _ = ref.route(np.full((1, 4), -np.inf), 2, "sigmoid")
+    assert idx.tolist() == [[-1, -1]]
+
+
+def test_structs_match_the_header():
+    import os
+    import re
+    h = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "moe.h")).read()
+    for name, cls in (("moe_route_config", moe._RouteConfig), ("moe_fp4_product", moe._Fp4Product)):
+        body = re.search(r"typedef struct \{([^{}]*)\} " + name, h).group(1)
+        body = re.sub(r"/\*.*?\*/", "", body, flags=re.S)
+        fields = [f.strip(" *\n") for line in body.split(";") for f in re.sub(r"^\s*(const )?\w+", "", line).split(",")]
+        assert [f for f in fields if f] == [n for n, _ in cls._fields_]
