@@ -529,9 +529,9 @@ MOE_API moe_status moe_dequantize_fp4(int32_t format, const uint8_t* codes, cons
  * y[t, n] = sum_k x[t, k] w[g, n, k] over the values that codes and scales stand for, accumulated
  * in fp32 and rounded once to y's type.
  *   x [T, K/2], w [E, N, K/2] codes, 16-byte aligned; K % 32 == 0
- *   x_scales, w_scales: K/32 or K/16 bytes per row, rows *_scale_stride bytes apart (where base and
- *          stride are multiples of 16 bytes, or of 8 for MXFP4, a row is read up to the next such
- *          boundary in one load: the last row must be readable that far)
+ *   x_scales, w_scales: K/32 or K/16 bytes per row, rows *_scale_stride bytes apart; base and
+ *          stride are multiples of 8 (MXFP4) or 16 (NVFP4) bytes (moe_fp4_pad_scales makes such
+ *          rows of others); nothing behind a row's last scale is read
  *   x_tensor_scale fp32 [1], w_tensor_scale fp32 [E] (device) or NULL; NVFP4 only
  *   offsets int32 [E + 1] device: rows offsets[g] .. offsets[g + 1] meet w[g]. Rows in none of
  *          these ranges (behind the last, in front of the first) are left as they were. Values are
@@ -556,6 +556,11 @@ typedef struct {
   void* y;
   int32_t* status;
 } moe_fp4_product;
+
+/* Scale rows [rows, cols] (contiguous) into rows dst_stride bytes apart (a multiple of 16, at least
+ * cols; dst 16-byte aligned), zeros behind them: for K whose scale rows are not aligned. */
+MOE_API moe_status moe_fp4_pad_scales(const uint8_t* src, int64_t rows, int32_t cols, uint8_t* dst,
+                                      int64_t dst_stride, moe_stream_t stream);
 
 MOE_API moe_status moe_fp4_matmul(const moe_fp4_product* p, moe_stream_t stream);
 

@@ -37,7 +37,7 @@ EXPORTED = ("moe_create", "moe_forward", "moe_forward_host", "moe_get_status", "
             "moe_set_hash_table", "moe_forward_hashed", "moe_fill_workspace", "moe_create_ep",
             "moe_forward_partial", "moe_read_bandwidth", "moe_forward_host_async", "moe_forward_host_wait",
             "moe_route", "moe_route_backward", "moe_forward_routed", "moe_quantize_fp4", "moe_dequantize_fp4",
-            "moe_fp4_matmul")
+            "moe_fp4_pad_scales", "moe_fp4_matmul")
 
 SCORES = {"softmax": 0, "sigmoid": 1, "sqrtsoftplus": 2}
 FP4_FORMATS = {"mxfp4": 0, "nvfp4": 1}
@@ -127,6 +127,7 @@ def lib() -> ctypes.CDLL:
             "moe_forward_routed": (I32, [P, P, P, P, I32, P, P]),
             "moe_quantize_fp4": (I32, [I32, P, I32, I64, I32, I64, P, P, P, I64, P]),
             "moe_dequantize_fp4": (I32, [I32, P, P, I64, I32, I64, P, P, I32, P]),
+            "moe_fp4_pad_scales": (I32, [P, I64, I32, P, I64, P]),
             "moe_fp4_matmul": (I32, [ctypes.POINTER(_Fp4Product), P]),
         }
         for name, (res, args) in sig.items():
@@ -400,10 +401,22 @@ def _fp4_out(x, T, N, out, out_dtype):
     return out
 
 
+def _aligned_scales(scales, f):
+    """(scales, row stride) with rows the product can read: as they are, or padded copies."""
+    cols = scales.shape[-1]
+    if (cols | scales.data_ptr()) % (16 if f else 8) == 0:
+        return scales, cols
+    rows, stride = scales.numel() // cols, (cols + 15) // 16 * 16
+    padded = torch.empty((rows, stride), dtype=torch.uint8, device=scales.device)
+    _check(lib().moe_fp4_pad_scales(scales.data_ptr(), rows, cols, padded.data_ptr(), stride, _current(scales)),
+           "moe_fp4_pad_scales")
+    return padded, stride
+
+
 def _fp4_product(f, x, x_scales, xss, x_ts, w, w_scales, w_ts, offsets, out, T, N, K, E, status):
+    w_scales, wss = _aligned_scales(w_scales, f)
     p = _Fp4Product(f, T, N, K, E, _VALUE_DTYPES[out.dtype], x.data_ptr(), x_scales.data_ptr(), xss, x_ts,
-                    w.data_ptr(), w_scales.data_ptr(), w_scales.shape[-1], w_ts, _addr(offsets), out.data_ptr(),
-                    _addr(status))
+                    w.data_ptr(), w_scales.data_ptr(), wss, w_ts, _addr(offsets), out.data_ptr(), _addr(status))
     _check(lib().moe_fp4_matmul(p, _current(x)), "moe_fp4_matmul")
     return out
 
@@ -442,7 +455,8 @@ def fp4_matmul(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_scale
         _need(status, "status", torch.int32, (1,))
     _same_device(x, x_scales=x_scales, w=w, w_scales=w_scales, x_tensor_scale=x_tensor_scale,
                  w_tensor_scale=w_tensor_scale, offsets=offsets, out=out, status=status)
-    return _fp4_product(f, x, x_scales, x_scales.shape[1], x_ts, w, w_scales, w_ts, offsets, out, T, N, K, E, status)
+    x_scales, xss = _aligned_scales(x_scales, f)
+    return _fp4_product(f, x, x_scales, xss, x_ts, w, w_scales, w_ts, offsets, out, T, N, K, E, status)
 
 
 def fp4_linear(x: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor, fmt: str, *,

@@ -259,6 +259,22 @@ __global__ void __launch_bounds__(256)
   store16<T>(dst + i * kRun, v, vec != 0);
 }
 
+// Scale rows into rows of another stride, 4 bytes of the destination per thread.
+__global__ void __launch_bounds__(256)
+    pad_scales_kernel(const uint8_t* __restrict__ src, int64_t words, int words_per_row, int cols,
+                      uint32_t* __restrict__ dst) {
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+  if (i >= words) return;
+  const int64_t row = i / words_per_row;
+  const int c = static_cast<int>(i - row * words_per_row) * 4;
+  const uint8_t* p = src + row * cols + c;
+  uint32_t w = 0u;
+#pragma unroll
+  for (int b = 0; b < 4; ++b)
+    if (c + b < cols) w |= static_cast<uint32_t>(__ldg(p + b)) << (8 * b);
+  dst[i] = w;
+}
+
 template <typename T, bool kNv>
 cudaError_t quantize_t(const void* src, int64_t rows, int cols, int64_t row_stride, const float* ts, uint8_t* codes,
                        uint8_t* scales, int64_t scale_stride, cudaStream_t s) {
@@ -298,6 +314,16 @@ cudaError_t launch_quantize_fp4(int format, const void* src, int dtype, int64_t 
   MOE_QUANT_CASE(kValFp32, float)
 #undef MOE_QUANT_CASE
   return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_pad_scales(const uint8_t* src, int64_t rows, int cols, uint8_t* dst, int64_t dst_stride,
+                              cudaStream_t s) {
+  if (rows == 0) return cudaSuccess;
+  const int wpr = static_cast<int>(dst_stride / 4);
+  const int64_t words = rows * wpr;
+  pad_scales_kernel<<<static_cast<unsigned>((words + 255) / 256), 256, 0, s>>>(src, words, wpr, cols,
+                                                                              reinterpret_cast<uint32_t*>(dst));
+  return cudaGetLastError();
 }
 
 cudaError_t launch_dequantize_fp4(int format, const uint8_t* codes, const uint8_t* scales, int64_t rows, int cols,

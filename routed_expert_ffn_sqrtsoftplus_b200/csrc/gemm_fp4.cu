@@ -11,12 +11,16 @@
 // MMAs and streams every weight byte once. Persistent CTAs, warp-specialised:
 //   warp 0      TMA: w box 256 values (128 bytes) x 128 kHalves rows, x boxes x 32 rows
 //   warp 1      issues the MMAs, four K = 64 steps per ring stage
-//   warps 2-5   scale factors, one warp per TMEM lane quarter: global memory -> registers
-//               (one stage ahead) -> TMEM with tcgen05.st. The MMA wants every row's
-//               scales in lane row % 32, column row / 32, replicated in the four quarters,
-//               which is how the four warps write them; nothing is rearranged beforehand
-//               and no shared memory is used
+//   warps 2-5   scale factors, one warp per TMEM lane quarter: shared memory -> registers ->
+//               TMEM with tcgen05.st. The MMA wants every row's scales in lane row % 32,
+//               column row / 32, replicated in the four quarters, which is how the four
+//               warps write them, so the scales stay in rows of K / 32 or K / 16 bytes in
+//               HBM and are rearranged nowhere
 //   warps 6-13  epilogue, two per lane quarter taking interleaved 16-column chunks
+//   warp 14     copies the scale rows of a stage into a ring of their own (cp.async, 16 or 8
+//               bytes a row, zeros where a row or its end is outside), several stages ahead:
+//               loaded by the warps that store them, one stage ahead, a load's latency set
+//               the time of a stage (T 8192, N 4608, K 5120: 650 us against 207 with this ring)
 //
 // Few tokens and few tiles: a cluster of `splits` CTAs takes one tile, each a slice of K;
 // the partial tiles meet in the first CTA's shared memory and are summed in slice order.
@@ -37,7 +41,8 @@ constexpr int kEpiWarps = 8;
 constexpr int kEpiGroups = kEpiWarps / 4;
 constexpr int kFirstSf = 2;
 constexpr int kFirstEpi = kFirstSf + kSfWarps;
-constexpr int kThreads = 32 * (kFirstEpi + kEpiWarps);
+constexpr int kSfLoader = kFirstEpi + kEpiWarps;
+constexpr int kThreads = 32 * (kSfLoader + 1);
 constexpr int kBK = 256;              // K values per stage
 constexpr int kRowBytes = kBK / 2;    // 128: one swizzle row
 constexpr int kBox = 32;              // token rows per TMA box
@@ -57,11 +62,14 @@ struct Cfg {
   static constexpr int kSets = (512 - kAccs * kAccCols) / kSfCols >= 4 ? 4 : (512 - kAccs * kAccCols) / kSfCols;
   static constexpr int kSfBase = kAccs * kAccCols;
   static constexpr int kFixed = 1024 + 512 + 2 * (kMaxExperts + 1) * 4;  // alignment, barriers, experts
-  static constexpr int kFit = (227 * 1024 - kFixed) / (kABytes + kBBytes);
+  static constexpr int kRowSf = kNv ? 16 : 8;                      // scale bytes of a row and stage
+  static constexpr int kRawBytes = (128 * kHalves + kBN) * kRowSf;
+  static constexpr int kRaw = 6;                                   // stages of scales in flight
+  static constexpr int kFit = (227 * 1024 - kFixed - kRaw * kRawBytes) / (kABytes + kBBytes);
   static constexpr int kStages = kFit > 8 ? 8 : kFit;
-  static constexpr int kSmemBytes = kFixed + kStages * (kABytes + kBBytes);
+  static constexpr int kSmemBytes = kFixed + kRaw * kRawBytes + kStages * (kABytes + kBBytes);
   static_assert(kSets >= 2, "scale factors of two stages");
-  static_assert((2 * kStages + 2 * kSets + 2 * kAccs + 1) * 8 + 8 <= 512, "barriers");
+  static_assert((2 * kStages + 2 * kSets + 2 * kAccs + 2 * kRaw + 1) * 8 + 8 <= 512, "barriers");
   // the partial tiles of a split fit in the ring (kHalves == 1, kBN == 32)
   static_assert(kHalves > 1 || kBN > 32 || (kMaxSplits - 1) * 128 * 32 * 4 <= kStages * (kABytes + kBBytes), "split");
 };
@@ -164,39 +172,31 @@ __device__ __forceinline__ Tile tile_of(int t, int E, int m_tiles, const int* pr
   return r;
 }
 
-// One row's scale words of a stage, zeros behind the row's end (what lies there may be NaN to the
-// MMA, which no zero code cancels). kVec: rows start 16 (E8M0: 8) bytes aligned and are readable
-// to that boundary; otherwise byte by byte.
-template <bool kNv, bool kVec>
-__device__ __forceinline__ void load_scales(const uint8_t* row, bool ok, int kb, int sf_cols, uint32_t* w) {
-  constexpr int kBytes = kNv ? 16 : 8;
-  constexpr int kWords = kBytes / 4;
-#pragma unroll
-  for (int j = 0; j < kWords; ++j) w[j] = 0u;
-  if (!ok) return;
-  const uint8_t* p = row + static_cast<size_t>(kb) * kBytes;
-  const int n = sf_cols - kb * kBytes;
-  if constexpr (kVec) {
-    if constexpr (kNv) {
-      const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
-      w[0] = v.x;
-      w[1] = v.y;
-      w[2] = v.z;
-      w[3] = v.w;
-    } else {
-      const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
-      w[0] = v.x;
-      w[1] = v.y;
-    }
-    if (n < kBytes) {
-#pragma unroll
-      for (int j = 0; j < kWords; ++j)
-        w[j] = n >= 4 * j + 4 ? w[j] : n <= 4 * j ? 0u : w[j] & ((1u << (8 * (n - 4 * j))) - 1u);
-    }
+// kBytes (8 or 16) to shared memory, the first n of them from global memory, zeros behind.
+template <int kBytes>
+__device__ __forceinline__ void cp_async_zfill(uint32_t dst, const void* src, int n) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)),
+               "n"(kBytes), "r"(n)
+               : "memory");
+}
+// Arrive on bar once this thread's copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// A row's kWords scale words of a stage, from shared memory.
+template <int kWords>
+__device__ __forceinline__ void read_scales(const uint8_t* p, uint32_t* w) {
+  if constexpr (kWords == 4) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    w[0] = v.x;
+    w[1] = v.y;
+    w[2] = v.z;
+    w[3] = v.w;
   } else {
-#pragma unroll
-    for (int b = 0; b < kBytes; ++b)
-      if (b < n) w[b / 4] |= static_cast<uint32_t>(__ldg(p + b)) << (8 * (b % 4));
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    w[0] = v.x;
+    w[1] = v.y;
   }
 }
 
@@ -237,23 +237,26 @@ __device__ __forceinline__ void store_any(const Fp4GemmArgs& a, int row0, int c0
     store_chunk<float>(a.out, a.N, row0, c0, nrows, n, n_ok, alpha, r);
 }
 
-template <bool kNv, int kHalves, int kBN, bool kVecW, bool kSplit>
+template <bool kNv, int kHalves, int kBN, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
-                    const Fp4GemmArgs args, const int vec_x) {
+                    const Fp4GemmArgs args) {
   using C = Cfg<kNv, kHalves, kBN>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sA = smem;
   uint8_t* sB = sA + C::kStages * C::kABytes;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sB + C::kStages * C::kBBytes);
+  uint8_t* sRaw = sB + C::kStages * C::kBBytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sRaw + C::kRaw * C::kRawBytes);
   uint64_t* full = bars;
   uint64_t* empty = full + C::kStages;
   uint64_t* sffull = empty + C::kStages;
   uint64_t* sfempty = sffull + C::kSets;
   uint64_t* tfull = sfempty + C::kSets;
   uint64_t* tempty = tfull + C::kAccs;
-  uint64_t* drain = tempty + C::kAccs;
+  uint64_t* rfull = tempty + C::kAccs;
+  uint64_t* rempty = rfull + C::kRaw;
+  uint64_t* drain = rempty + C::kRaw;
   uint32_t* tmem_base_smem = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_base_smem + 1);
   int* pre = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(bars) + 512);  // [E + 1] first token tile
@@ -274,6 +277,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < C::kAccs; ++i) {
       mbar_init(&tfull[i], 1);
       mbar_init(&tempty[i], kEpiWarps);
+    }
+    for (int i = 0; i < C::kRaw; ++i) {
+      mbar_init(&rfull[i], 32);
+      mbar_init(&rempty[i], kSfWarps);
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -427,91 +434,101 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp < kFirstEpi) {
-    // ------------------------------------------------------------ scale factors
+    // ------------------------------------------------------------ scale factors -> TMEM
     constexpr int kW = C::kAtoms;
     constexpr int kARows = 4 * kHalves, kBRows = kBN / 32;  // rows of this lane: 32 apart
     const uint32_t quarter = tmem_base + (static_cast<uint32_t>((warp & 3) * 32) << 16) + C::kSfBase;
-    uint32_t cur[(kARows + kBRows) * kW], nxt[(kARows + kBRows) * kW];
-    int t = t0, kb = kb0, set = 0;
-    uint32_t sphase = 0;
-    const uint8_t* wrow = nullptr;
-    const uint8_t* xrow = nullptr;
-    int w_left = 0, x_left = 0;  // rows of the tile from this lane's first one
-    auto open = [&]() {
-      const Tile tl = tile_of<kBN>(t, args.E, args.m_tiles, pre, row_s);
-      const int n = tl.m * 128 * kHalves + lane;
-      w_left = args.N - n;
-      x_left = tl.nrows - lane;
-      wrow = args.ws + (static_cast<int64_t>(tl.g) * args.N + n) * args.ws_stride;
-      xrow = args.xs + static_cast<int64_t>(tl.row0 + lane) * args.xs_stride;
-    };
-    auto fetch = [&](uint32_t* w) {
+    int set = 0, raw = 0;
+    uint32_t sphase = 0, rphase = 0;
+    bool ok = true;
+    for (int t = t0; ok && t < total; t += stride) {
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (lane == 0)
+          ok = wait_or_abort(&rfull[raw], rphase, args, abort_flag) &&
+               wait_or_abort(&sfempty[set], sphase ^ 1, args, abort_flag);
+        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        if (!ok) break;
+        tc_fence_after();
+        const uint8_t* src = sRaw + raw * C::kRawBytes + lane * C::kRowSf;
+        const uint32_t base = quarter + set * C::kSfCols;
 #pragma unroll
-      for (int i = 0; i < kARows; ++i)
-        load_scales<kNv, kVecW>(wrow + static_cast<int64_t>(i) * 32 * args.ws_stride, i * 32 < w_left, kb,
-                                args.sf_cols, w + i * kW);
-      if (vec_x) {
+        for (int h = 0; h < kHalves; ++h) {
+          uint32_t w[4 * kW];
 #pragma unroll
-        for (int i = 0; i < kBRows; ++i)
-          load_scales<kNv, true>(xrow + static_cast<int64_t>(i) * 32 * args.xs_stride, i * 32 < x_left, kb,
-                                 args.sf_cols, w + (kARows + i) * kW);
-      } else {
+          for (int i = 0; i < 4; ++i) read_scales<kW>(src + (4 * h + i) * 32 * C::kRowSf, w + i * kW);
 #pragma unroll
-        for (int i = 0; i < kBRows; ++i)
-          load_scales<kNv, false>(xrow + static_cast<int64_t>(i) * 32 * args.xs_stride, i * 32 < x_left, kb,
-                                  args.sf_cols, w + (kARows + i) * kW);
-      }
-    };
-    auto advance = [&]() {  // to the next stage; false behind the last
-      if (++kb == kb1) {
-        kb = kb0;
-        t += stride;
-        if (t >= total) return false;
-        open();
-      }
-      return true;
-    };
-    bool more = t < total && kb0 < kb1;
-    if (more) {
-      open();
-      fetch(cur);
-    }
-    while (more) {
-      more = advance();
-      if (more) fetch(nxt);
-      bool ok = true;
-      if (lane == 0) ok = wait_or_abort(&sfempty[set], sphase ^ 1, args, abort_flag);
-      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-      if (!ok) break;
-      tc_fence_after();
-      const uint32_t base = quarter + set * C::kSfCols;
-#pragma unroll
-      for (int h = 0; h < kHalves; ++h)
-#pragma unroll
-        for (int j = 0; j < kW; ++j) {
-          const uint32_t* w = cur + h * 4 * kW + j;
-          tmem_st4(base + (h * kW + j) * 4, w[0], w[kW], w[2 * kW], w[3 * kW]);
+          for (int j = 0; j < kW; ++j) tmem_st4(base + (h * kW + j) * 4, w[j], w[kW + j], w[2 * kW + j], w[3 * kW + j]);
         }
-#pragma unroll
-      for (int j = 0; j < kW; ++j)
 #pragma unroll
         for (int c = 0; c < C::kBCols; c += 4) {
-          uint32_t v[4];
+          uint32_t w[4 * kW];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] = c + i < kBRows ? cur[(kARows + (c + i < kBRows ? c + i : 0)) * kW + j] : 0u;
-          tmem_st4(base + kHalves * kW * 4 + j * C::kBCols + c, v[0], v[1], v[2], v[3]);
+          for (int i = 0; i < 4 * kW; ++i) w[i] = 0u;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (c + i < kBRows) read_scales<kW>(src + (kARows + c + i) * 32 * C::kRowSf, w + i * kW);
+#pragma unroll
+          for (int j = 0; j < kW; ++j)
+            tmem_st4(base + kHalves * kW * 4 + j * C::kBCols + c, w[j], w[kW + j], w[2 * kW + j], w[3 * kW + j]);
         }
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sffull[set]);
-      if (++set == C::kSets) {
-        set = 0;
-        sphase ^= 1;
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&rempty[raw]);
+          mbar_arrive(&sffull[set]);
+        }
+        if (++set == C::kSets) {
+          set = 0;
+          sphase ^= 1;
+        }
+        if (++raw == C::kRaw) {
+          raw = 0;
+          rphase ^= 1;
+        }
       }
-#pragma unroll
-      for (int i = 0; i < (kARows + kBRows) * kW; ++i) cur[i] = nxt[i];
     }
+  } else if (warp == kSfLoader) {
+    // ------------------------------------------------------------ scale rows -> shared memory
+    constexpr int kB = C::kRowSf;
+    int raw = 0;
+    uint32_t rphase = 0;
+    bool ok = true;
+    for (int t = t0; ok && t < total; t += stride) {
+      const Tile tl = tile_of<kBN>(t, args.E, args.m_tiles, pre, row_s);
+      const int n = tl.m * 128 * kHalves + lane;
+      const int w_left = args.N - n, x_left = tl.nrows - lane;  // rows from this lane's first one
+      const uint8_t* wrow = args.ws + (static_cast<int64_t>(tl.g) * args.N + n) * args.ws_stride;
+      const uint8_t* xrow = args.xs + static_cast<int64_t>(tl.row0 + lane) * args.xs_stride;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (lane == 0) ok = wait_or_abort(&rempty[raw], rphase ^ 1, args, abort_flag);
+        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        if (!ok) break;
+        const uint32_t dst = smem_u32(sRaw + raw * C::kRawBytes + lane * kB);
+        const int off = kb * kB;
+        const int left = min(kB, args.sf_cols - off);
+        // a row outside reads nothing (0 bytes from the scales' own start)
+#pragma unroll
+        for (int i = 0; i < 4 * kHalves; ++i) {
+          const bool in = 32 * i < w_left;
+          cp_async_zfill<kB>(dst + i * 32 * kB, in ? wrow + static_cast<int64_t>(i) * 32 * args.ws_stride + off : args.ws,
+                             in ? left : 0);
+        }
+#pragma unroll
+        for (int i = 0; i < kBN / 32; ++i) {
+          const bool in = 32 * i < x_left;
+          cp_async_zfill<kB>(dst + (4 * kHalves + i) * 32 * kB,
+                             in ? xrow + static_cast<int64_t>(i) * 32 * args.xs_stride + off : args.xs, in ? left : 0);
+        }
+        cp_async_arrive(&rfull[raw]);
+        if (++raw == C::kRaw) {
+          raw = 0;
+          rphase ^= 1;
+        }
+      }
+    }
+    // copies in flight land before the CTA's shared memory goes
+    asm volatile("cp.async.wait_all;" ::: "memory");
   } else {
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;
@@ -557,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     cluster_sync_all();
     const int q = warp & 3;
     const int cfirst = ((warp - kFirstEpi) / 4) * 16;
-    const bool work = warp >= kFirstEpi && t0 < total && !*abort_flag;
+    const bool work = warp >= kFirstEpi && warp < kSfLoader && t0 < total && !*abort_flag;
     Tile tl{};
     if (work) tl = tile_of<kBN>(t0, args.E, args.m_tiles, pre, row_s);
     uint32_t r[16];
@@ -593,11 +610,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <bool kNv, int kHalves, int kBN, bool kVecW, bool kSplit>
-cudaError_t launch_cfg(const CUtensorMap& tw, const CUtensorMap& tx, const Fp4GemmArgs& a, int grid, bool vec_x,
-                       cudaStream_t s) {
+template <bool kNv, int kHalves, int kBN, bool kSplit>
+cudaError_t launch_cfg(const CUtensorMap& tw, const CUtensorMap& tx, const Fp4GemmArgs& a, int grid, cudaStream_t s) {
   using C = Cfg<kNv, kHalves, kBN>;
-  auto* kernel = gemm_fp4_kernel<kNv, kHalves, kBN, kVecW, kSplit>;
+  auto* kernel = gemm_fp4_kernel<kNv, kHalves, kBN, kSplit>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
@@ -611,22 +627,22 @@ cudaError_t launch_cfg(const CUtensorMap& tw, const CUtensorMap& tx, const Fp4Ge
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = kSplit ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kernel, tw, tx, a, vec_x ? 1 : 0);
+  return cudaLaunchKernelEx(&cfg, kernel, tw, tx, a);
 }
 
-template <bool kNv, bool kVecW>
+template <bool kNv>
 cudaError_t launch_fmt(const CUtensorMap& tw, const CUtensorMap& tx, const Fp4GemmArgs& a, const Fp4Plan& p,
-                       int num_sms, bool vec_x, cudaStream_t s) {
+                       int num_sms, cudaStream_t s) {
   // token tiles: at most T / bn whole ones, and one partial one for each expert that has rows
   const int64_t tok = a.E == 1 ? (a.T + p.bn - 1) / p.bn : a.T / p.bn + (a.E < a.T ? a.E : a.T);
   const int64_t most = tok * a.m_tiles;
   if (p.splits > 1)
-    return launch_cfg<kNv, 1, 32, kVecW, true>(tw, tx, a, static_cast<int>(most) * p.splits, vec_x, s);
+    return launch_cfg<kNv, 1, 32, true>(tw, tx, a, static_cast<int>(most) * p.splits, s);
   const int grid = static_cast<int>(most < num_sms ? most : num_sms);
-  if (p.halves == 1) return launch_cfg<kNv, 1, 32, kVecW, false>(tw, tx, a, grid, vec_x, s);
-  if (p.bn == 32) return launch_cfg<kNv, 2, 32, kVecW, false>(tw, tx, a, grid, vec_x, s);
-  if (p.bn == 96) return launch_cfg<kNv, 2, 96, kVecW, false>(tw, tx, a, grid, vec_x, s);
-  return launch_cfg<kNv, 2, 192, kVecW, false>(tw, tx, a, grid, vec_x, s);
+  if (p.halves == 1) return launch_cfg<kNv, 1, 32, false>(tw, tx, a, grid, s);
+  if (p.bn == 32) return launch_cfg<kNv, 2, 32, false>(tw, tx, a, grid, s);
+  if (p.bn == 96) return launch_cfg<kNv, 2, 96, false>(tw, tx, a, grid, s);
+  return launch_cfg<kNv, 2, 192, false>(tw, tx, a, grid, s);
 }
 
 }  // namespace
@@ -656,14 +672,7 @@ Fp4Plan fp4_plan(int T, int N, int E, int num_kb, int num_sms) {
 cudaError_t launch_gemm_fp4(int format, const CUtensorMap& tw, const CUtensorMap& tx, const Fp4GemmArgs& a,
                             const Fp4Plan& p, int num_sms, cudaStream_t s) {
   if (a.E > kMaxExperts) return cudaErrorInvalidValue;
-  const int unit = format == kFp4Nv ? 16 : 8;
-  auto vec = [&](const uint8_t* base, int64_t stride) {
-    return reinterpret_cast<uintptr_t>(base) % unit == 0 && stride % unit == 0;
-  };
-  const bool vw = vec(a.ws, a.ws_stride), vx = vec(a.xs, a.xs_stride);
-  if (format == kFp4Nv)
-    return vw ? launch_fmt<true, true>(tw, tx, a, p, num_sms, vx, s) : launch_fmt<true, false>(tw, tx, a, p, num_sms, vx, s);
-  return vw ? launch_fmt<false, true>(tw, tx, a, p, num_sms, vx, s) : launch_fmt<false, false>(tw, tx, a, p, num_sms, vx, s);
+  return format == kFp4Nv ? launch_fmt<true>(tw, tx, a, p, num_sms, s) : launch_fmt<false>(tw, tx, a, p, num_sms, s);
 }
 
 }  // namespace moe

@@ -347,6 +347,9 @@ cudaError_t launch_quantize_fp4(int format, const void* src, int dtype, int64_t 
 cudaError_t launch_dequantize_fp4(int format, const uint8_t* codes, const uint8_t* scales, int64_t rows, int cols,
                                   int64_t scale_stride, const float* tensor_scale, void* dst, int dtype,
                                   cudaStream_t s);
+// Scale rows [rows, cols] into rows dst_stride bytes apart (a multiple of 4, at least cols), zeros behind.
+cudaError_t launch_pad_scales(const uint8_t* src, int64_t rows, int cols, uint8_t* dst, int64_t dst_stride,
+                              cudaStream_t s);
 // y[t, n] = alpha sum_k x[t, k] w[g(t), n, k]; see gemm_fp4.cu
 struct Fp4GemmArgs {
   const uint8_t* xs;            // scales of x, rows xs_stride bytes apart

@@ -150,20 +150,35 @@ moe_status moe_dequantize_fp4(int32_t format, const uint8_t* codes, const uint8_
                                         as_stream(stream)));
 }
 
+moe_status moe_fp4_pad_scales(const uint8_t* src, int64_t rows, int32_t cols, uint8_t* dst, int64_t dst_stride,
+                              moe_stream_t stream) {
+  if (rows < 0 || cols < 1 || dst_stride < cols || dst_stride % 16 != 0) return MOE_ERR_INVALID_ARG;
+  if (dst_stride > 1 << 20 || rows > (int64_t(1) << 38) / dst_stride) return MOE_ERR_UNSUPPORTED;
+  if (rows == 0) return MOE_OK;
+  if (src == nullptr || dst == nullptr || !aligned(dst, 16)) return MOE_ERR_INVALID_ARG;
+  const moe_status st = on_device({src, dst});
+  if (st != MOE_OK) return st;
+  return launched(launch_pad_scales(src, rows, cols, dst, dst_stride, as_stream(stream)));
+}
+
 moe_status moe_fp4_matmul(const moe_fp4_product* p, moe_stream_t stream) {
   if (p == nullptr || !fp4_format_ok(p->format)) return MOE_ERR_INVALID_ARG;
   if (p->T < 0 || p->N < 1 || p->K < 1 || p->E < 1 || p->K % 32 != 0 || value_bytes(p->out_dtype) == 0)
     return MOE_ERR_INVALID_ARG;
   if (p->offsets == nullptr && p->E != 1) return MOE_ERR_INVALID_ARG;
   const int cols = p->K / (p->format == MOE_FP4_NV ? 16 : 32);
-  if (p->x_scale_stride < cols || p->w_scale_stride < cols) return MOE_ERR_INVALID_ARG;
+  const int unit = p->format == MOE_FP4_NV ? 16 : 8;
+  if (p->x_scale_stride < cols || p->w_scale_stride < cols || p->x_scale_stride % unit != 0 ||
+      p->w_scale_stride % unit != 0)
+    return MOE_ERR_INVALID_ARG;
   if (p->format == MOE_FP4_MX && (p->x_tensor_scale != nullptr || p->w_tensor_scale != nullptr))
     return MOE_ERR_INVALID_ARG;
   if (p->T > 1 << 22 || p->N > 1 << 18 || p->K > 1 << 18 || p->E > 512) return MOE_ERR_UNSUPPORTED;
   if (p->T == 0) return MOE_OK;
   if (p->x == nullptr || p->x_scales == nullptr || p->w == nullptr || p->w_scales == nullptr || p->y == nullptr)
     return MOE_ERR_INVALID_ARG;
-  if (!aligned(p->x, 16) || !aligned(p->w, 16) || !aligned(p->y, value_bytes(p->out_dtype)) ||
+  if (!aligned(p->x, 16) || !aligned(p->w, 16) || !aligned(p->x_scales, unit) || !aligned(p->w_scales, unit) ||
+      !aligned(p->y, value_bytes(p->out_dtype)) ||
       !aligned(p->offsets, 4) || !aligned(p->x_tensor_scale, 4) || !aligned(p->w_tensor_scale, 4) ||
       !aligned(p->status, 4))
     return MOE_ERR_INVALID_ARG;

@@ -73,18 +73,23 @@ def test_fp4_refuses_bad_arguments(L):
     assert d(1, FAKE, FAKE, 4, 40, 4, None, FAKE, 0, None) == INV
     assert d(0, FAKE, FAKE, 4, 64, 2, FAKE, FAKE, 0, None) == INV
     assert d(0, None, None, 0, 64, 2, None, None, 0, None) == OK
+    p = L.moe_fp4_pad_scales
+    assert p(FAKE, 4, 20, FAKE, 16, None) == INV and p(FAKE, 4, 20, FAKE, 24, None) == INV
+    assert p(FAKE, 4, 20, FAKE + 4, 32, None) == INV and p(None, 4, 20, FAKE, 32, None) == INV
+    assert p(FAKE, 4, 0, FAKE, 32, None) == INV and p(None, 0, 20, None, 32, None) == OK
 
 
 def _product(**kw):
-    d = dict(format=0, T=4, N=64, K=64, E=1, out_dtype=0, x=FAKE, x_scales=FAKE, x_scale_stride=2, x_tensor_scale=None,
-             w=FAKE, w_scales=FAKE, w_scale_stride=2, w_tensor_scale=None, offsets=None, y=FAKE, status=None)
+    d = dict(format=0, T=4, N=64, K=64, E=1, out_dtype=0, x=FAKE, x_scales=FAKE, x_scale_stride=8, x_tensor_scale=None,
+             w=FAKE, w_scales=FAKE, w_scale_stride=8, w_tensor_scale=None, offsets=None, y=FAKE, status=None)
     d.update(kw)
     return moe._Fp4Product(*[d[n] for n, _ in moe._Fp4Product._fields_])
 
 
 @pytest.mark.parametrize("kw,want", [
     (dict(format=2), INV), (dict(T=-1), INV), (dict(N=0), INV), (dict(K=48), INV), (dict(K=0), INV), (dict(E=0), INV),
-    (dict(E=2), INV), (dict(out_dtype=3), INV), (dict(x_scale_stride=1), INV), (dict(format=1), INV),
+    (dict(E=2), INV), (dict(out_dtype=3), INV), (dict(x_scale_stride=1), INV), (dict(format=1), INV), (dict(w_scale_stride=12), INV),
+    (dict(K=512), INV), (dict(x_scales=FAKE + 4), INV), (dict(format=1, x_scale_stride=16, w_scale_stride=16, w_scales=FAKE + 8), INV),
     (dict(x_tensor_scale=FAKE), INV), (dict(w_tensor_scale=FAKE), INV), (dict(x=None), INV), (dict(w=FAKE + 8), INV),
     (dict(x=FAKE + 4), INV), (dict(y=FAKE + 1), INV), (dict(y=None), INV), (dict(w_scales=None), INV),
     (dict(offsets=FAKE + 2), INV), (dict(T=(1 << 22) + 1), UNS), (dict(E=513, offsets=FAKE), UNS),
