@@ -37,7 +37,7 @@ EXPORTED = ("moe_create", "moe_forward", "moe_forward_host", "moe_get_status", "
             "moe_set_hash_table", "moe_forward_hashed", "moe_fill_workspace", "moe_create_ep",
             "moe_forward_partial", "moe_read_bandwidth", "moe_forward_host_async", "moe_forward_host_wait",
             "moe_route", "moe_route_backward", "moe_forward_routed", "moe_quantize_fp4", "moe_dequantize_fp4",
-            "moe_fp4_pad_scales", "moe_fp4_matmul")
+            "moe_fp4_pad_scales", "moe_fp4_workspace_bytes", "moe_fp4_matmul")
 
 SCORES = {"softmax": 0, "sigmoid": 1, "sqrtsoftplus": 2}
 FP4_FORMATS = {"mxfp4": 0, "nvfp4": 1}
@@ -79,7 +79,8 @@ class _Fp4Product(ctypes.Structure):
                 [("x", ctypes.c_void_p), ("x_scales", ctypes.c_void_p), ("x_scale_stride", ctypes.c_int64),
                  ("x_tensor_scale", ctypes.c_void_p), ("w", ctypes.c_void_p), ("w_scales", ctypes.c_void_p),
                  ("w_scale_stride", ctypes.c_int64)] +
-                [(n, ctypes.c_void_p) for n in ("w_tensor_scale", "offsets", "y", "status")])
+                [(n, ctypes.c_void_p) for n in ("w_tensor_scale", "offsets", "y", "workspace")] +
+                [("workspace_bytes", ctypes.c_int64), ("status", ctypes.c_void_p)])
 
 
 _lib = None
@@ -128,6 +129,7 @@ def lib() -> ctypes.CDLL:
             "moe_quantize_fp4": (I32, [I32, P, I32, I64, I32, I64, P, P, P, I64, P]),
             "moe_dequantize_fp4": (I32, [I32, P, P, I64, I32, I64, P, P, I32, P]),
             "moe_fp4_pad_scales": (I32, [P, I64, I32, P, I64, P]),
+            "moe_fp4_workspace_bytes": (I64, [I32, I32, I32, I32, I32]),
             "moe_fp4_matmul": (I32, [ctypes.POINTER(_Fp4Product), P]),
         }
         for name, (res, args) in sig.items():
@@ -402,7 +404,7 @@ def _fp4_out(x, T, N, out, out_dtype):
 
 
 def _aligned_scales(scales, f):
-    """(scales, row stride) with rows the product can read: as they are, or padded copies."""
+    """(scales, row stride) with rows that a product of few rows can read: as they are, or padded copies."""
     cols = scales.shape[-1]
     if (cols | scales.data_ptr()) % (16 if f else 8) == 0:
         return scales, cols
@@ -414,10 +416,19 @@ def _aligned_scales(scales, f):
 
 
 def _fp4_product(f, x, x_scales, xss, x_ts, w, w_scales, w_ts, offsets, out, T, N, K, E, status):
-    w_scales, wss = _aligned_scales(w_scales, f)
+    L = lib()
+    wss, space, nbytes = w_scales.shape[-1], None, 0
+    if T <= 32 * E:       # few rows: no workspace, but aligned rows of scales
+        w_scales, wss = _aligned_scales(w_scales, f)
+        if xss == x_scales.shape[-1]:
+            x_scales, xss = _aligned_scales(x_scales, f)
+    else:
+        nbytes = L.moe_fp4_workspace_bytes(f, T, N, K, E)
+        space = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
     p = _Fp4Product(f, T, N, K, E, _VALUE_DTYPES[out.dtype], x.data_ptr(), x_scales.data_ptr(), xss, x_ts,
-                    w.data_ptr(), w_scales.data_ptr(), wss, w_ts, _addr(offsets), out.data_ptr(), _addr(status))
-    _check(lib().moe_fp4_matmul(p, _current(x)), "moe_fp4_matmul")
+                    w.data_ptr(), w_scales.data_ptr(), wss, w_ts, _addr(offsets), out.data_ptr(), _addr(space), nbytes,
+                    _addr(status))
+    _check(L.moe_fp4_matmul(p, _current(x)), "moe_fp4_matmul")
     return out
 
 
@@ -455,8 +466,7 @@ def fp4_matmul(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_scale
         _need(status, "status", torch.int32, (1,))
     _same_device(x, x_scales=x_scales, w=w, w_scales=w_scales, x_tensor_scale=x_tensor_scale,
                  w_tensor_scale=w_tensor_scale, offsets=offsets, out=out, status=status)
-    x_scales, xss = _aligned_scales(x_scales, f)
-    return _fp4_product(f, x, x_scales, xss, x_ts, w, w_scales, w_ts, offsets, out, T, N, K, E, status)
+    return _fp4_product(f, x, x_scales, x_scales.shape[1], x_ts, w, w_scales, w_ts, offsets, out, T, N, K, E, status)
 
 
 def fp4_linear(x: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor, fmt: str, *,

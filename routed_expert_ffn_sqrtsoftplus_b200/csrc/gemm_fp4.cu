@@ -9,18 +9,21 @@
 // As in the layer's GEMMs the weights are the M operand (128 rows per MMA, kHalves MMAs
 // sharing the token tile) and the tokens are N, so that one token still issues full-height
 // MMAs and streams every weight byte once. Persistent CTAs, warp-specialised:
-//   warp 0      TMA: w box 256 values (128 bytes) x 128 kHalves rows, x boxes x 32 rows
-//   warp 1      issues the MMAs, four K = 64 steps per ring stage
-//   warps 2-5   scale factors, one warp per TMEM lane quarter: shared memory -> registers ->
-//               TMEM with tcgen05.st. The MMA wants every row's scales in lane row % 32,
-//               column row / 32, replicated in the four quarters, which is how the four
-//               warps write them, so the scales stay in rows of K / 32 or K / 16 bytes in
-//               HBM and are rearranged nowhere
-//   warps 6-13  epilogue, two per lane quarter taking interleaved 16-column chunks
-//   warp 14     copies the scale rows of a stage into a ring of their own (cp.async, 16 or 8
-//               bytes a row, zeros where a row or its end is outside), several stages ahead:
-//               loaded by the warps that store them, one stage ahead, a load's latency set
-//               the time of a stage (T 8192, N 4608, K 5120: 650 us against 207 with this ring)
+//   warp 0      TMA: a box of 256 values (128 bytes) x 128 kHalves rows of w, boxes of 32 rows of x
+//   warp 1      copies a stage's scale factors to TMEM (tcgen05.cp) and issues its MMAs, four
+//               K = 64 steps per ring stage
+//   the others  epilogue, two or three per lane quarter taking interleaved 16-column chunks
+//
+// The MMA wants the scales of 128 rows as words of four K blocks, row r at 16 (r % 32) + 4 (r / 32),
+// where HBM has rows of K / 32 or K / 16 bytes.
+//   kPre = false (32-token tiles, bound by HBM): warp 14 brings a stage's scale rows into a ring of
+//     their own (cp.async, 16 or 8 bytes a row, zeros outside), warps 2-5 turn them in place (lane l
+//     takes rows l, l + 32, l + 64, l + 96). The weights' scales are read once, from where they are.
+//   kPre = true (more tokens, bound by shared memory's bandwidth): a kernel in front arranges both
+//     operands' scales into a workspace, and they come with the tiles, two bulk copies a stage.
+//     Turned in the kernel they cost 24 KB of shared-memory traffic a stage by the LSUs, behind
+//     MMAs that already read 107 of 128 bytes a cycle: turning a stage took 1000 to 3000 cycles
+//     where its MMAs take 768.
 //
 // Few tokens and few tiles: a cluster of `splits` CTAs takes one tile, each a slice of K;
 // the partial tiles meet in the first CTA's shared memory and are summed in slice order.
@@ -28,6 +31,8 @@
 // Every read of offsets is clamped to [0, T] and to ascending order, so no offsets lead
 // outside x or y. All waits are bounded.
 #include <cuda_fp16.h>
+
+#include <atomic>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -37,11 +42,8 @@ namespace moe {
 namespace {
 
 constexpr int kSfWarps = 4;
-constexpr int kEpiWarps = 8;
-constexpr int kEpiGroups = kEpiWarps / 4;
 constexpr int kFirstSf = 2;
-constexpr int kFirstEpi = kFirstSf + kSfWarps;
-constexpr int kSfLoader = kFirstEpi + kEpiWarps;
+constexpr int kSfLoader = 14;
 constexpr int kThreads = 32 * (kSfLoader + 1);
 constexpr int kBK = 256;              // K values per stage
 constexpr int kRowBytes = kBK / 2;    // 128: one swizzle row
@@ -49,67 +51,87 @@ constexpr int kBox = 32;              // token rows per TMA box
 constexpr int kMaxExperts = 512;
 constexpr int kMaxSplits = 8;
 
-// kHalves: 128-row halves of w per tile; kBN: token rows per tile.
-template <bool kNv, int kHalves, int kBN>
+// kHalves: 128-row halves of w per tile; kBN: rows of x per tile.
+template <bool kNv, bool kPre, int kHalves, int kBN>
 struct Cfg {
   static constexpr int kABytes = kHalves * 128 * kRowBytes;
   static constexpr int kBBytes = kBN * kRowBytes;
+  static constexpr int kTokens = kBN;
+  static constexpr int kCols = 128 * kHalves;                      // rows of w, columns of y
+  static constexpr int kFirstEpi = kPre ? kFirstSf : kFirstSf + kSfWarps;
+  static constexpr int kEpiWarps = kPre ? 12 : 8;
+  static constexpr int kEpiGroups = kEpiWarps / 4;
   static constexpr int kAtoms = kNv ? 4 : 2;                       // 32-bit words of scales per row and stage
-  static constexpr int kBCols = (kBN / 32 + 3) / 4 * 4;            // TMEM columns of one atom of x's scales
-  static constexpr int kSfCols = kAtoms * (4 * kHalves + kBCols);  // ... of one stage's scales
+  static constexpr int kBBlocks = (kBN + 127) / 128;               // 128-row blocks of x's scales
+  static constexpr int kBCols = kBBlocks * 4;                      // TMEM columns of one word of them
+  static constexpr int kSfCols = kAtoms * (4 * kHalves + kBCols);  // TMEM columns of one stage's scales
   static constexpr int kAccCols = kHalves * kBN;
   static constexpr int kAccs = 2 * kAccCols + 2 * kSfCols <= 512 ? 2 : 1;
-  static constexpr int kSets = (512 - kAccs * kAccCols) / kSfCols >= 4 ? 4 : (512 - kAccs * kAccCols) / kSfCols;
   static constexpr int kSfBase = kAccs * kAccCols;
-  static constexpr int kFixed = 1024 + 512 + 2 * (kMaxExperts + 1) * 4;  // alignment, barriers, experts
+  static constexpr int kSets = kSfBase + 3 * kSfCols <= 512 ? 3 : 2;  // stages whose scales TMEM holds
   static constexpr int kRowSf = kNv ? 16 : 8;                      // scale bytes of a row and stage
-  static constexpr int kRawBytes = (128 * kHalves + kBN) * kRowSf;
-  static constexpr int kRaw = 6;                                   // stages of scales in flight
-  static constexpr int kFit = (227 * 1024 - kFixed - kRaw * kRawBytes) / (kABytes + kBBytes);
+  static constexpr int kBlocks = kHalves + kBBlocks;
+  static constexpr int kBlockBytes = 128 * kRowSf;
+  static constexpr int kRawBytes = kBlocks * kBlockBytes;
+  static constexpr int kASfBytes = kHalves * kAtoms * 512, kBSfBytes = kBBlocks * kAtoms * 512;  // = kRawBytes
+  static constexpr int kFixed = 1024 + 512 + 2 * (kMaxExperts + 1) * 4;  // alignment, barriers, experts
+  // stages of scales in flight: as the tiles' where they come together, else six
+  static constexpr int kFit = kPre ? (227 * 1024 - kFixed) / (kABytes + kBBytes + kRawBytes)
+                                   : (227 * 1024 - kFixed - 6 * kRawBytes) / (kABytes + kBBytes);
   static constexpr int kStages = kFit > 8 ? 8 : kFit;
+  static constexpr int kRaw = kPre ? kStages : 6;
   static constexpr int kSmemBytes = kFixed + kRaw * kRawBytes + kStages * (kABytes + kBBytes);
-  static_assert(kSets >= 2, "scale factors of two stages");
-  static_assert((2 * kStages + 2 * kSets + 2 * kAccs + 2 * kRaw + 1) * 8 + 8 <= 512, "barriers");
+  static_assert(kSfBase + kSets * kSfCols <= 512 && kSets <= kRaw && kStages >= 2, "TMEM, ring");
+  static_assert((2 * kStages + 3 * kRaw + 2 * kAccs + 1) * 8 + 8 <= 512, "barriers");
   // the partial tiles of a split fit in the ring (kHalves == 1, kBN == 32)
   static_assert(kHalves > 1 || kBN > 32 || (kMaxSplits - 1) * 128 * 32 * 4 <= kStages * (kABytes + kBBytes), "split");
 };
 
 // Instruction descriptor of the 4-bit kinds: E2M1 is format 1 (A bits 7-9, B bits 10-12), both
 // K-major, N >> 3 in bits 17-22, scale format in bit 23 (1: E8M0, 0: E4M3), M >> 4 in bits 24-28,
-// scale-factor ids in bits 4-5 (B) and 29-30 (A), K = 64 (bit 31 = 0).
-__device__ __forceinline__ uint32_t idesc_fp4(bool nv, uint32_t N, uint32_t sf_id) {
-  return (sf_id << 4) | (1u << 7) | (1u << 10) | ((N >> 3) << 17) | ((nv ? 0u : 1u) << 23) | ((128u >> 4) << 24) |
-         (sf_id << 29);
+// scale-factor ids in bits 4-5 (B) and 29-30 (A), both set by the caller, K = 64 (bit 31 = 0).
+__device__ __forceinline__ uint32_t idesc_fp4(bool nv, uint32_t N) {
+  return (1u << 7) | (1u << 10) | ((N >> 3) << 17) | ((nv ? 0u : 1u) << 23) | ((128u >> 4) << 24);
 }
 
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(p));
+  return p != 0;
+}
+
+// The descriptors' high halves (layout, strides) are the same everywhere; the low ones hold the
+// address.
 template <bool kNv>
-__device__ __forceinline__ void umma_fp4(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t sfa,
-                                         uint32_t sfb, uint32_t accumulate) {
+__device__ __forceinline__ void umma_fp4(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc,
+                                         uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
   if constexpr (kNv)
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%5], [%6], p;\n\t}\n" ::
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], a, b, %4, [%6], [%7], p;\n\t}\n" ::
             "r"(d),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb)
+        "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb)
         : "memory");
   else
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}\n" ::"r"(
-            d),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb)
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], a, b, %4, [%6], [%7], p;\n\t}\n" ::"r"(d),
+        "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb)
         : "memory");
 }
-
-// Four consecutive 32-bit TMEM columns of this warp's lane quarter.
-__device__ __forceinline__ void tmem_st4(uint32_t taddr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(a), "r"(b), "r"(c),
-               "r"(d)
-               : "memory");
+// tmem_cp_32x128b_x4 with the descriptor in halves.
+__device__ __forceinline__ void copy_word(uint32_t taddr, uint32_t lo, uint32_t hi) {
+  asm volatile(
+      "{\n\t.reg .b64 s;\n\tmov.b64 s, {%1, %2};\n\ttcgen05.cp.cta_group::1.32x128b.warpx4 [%0], s;\n\t}\n" ::"r"(
+          taddr),
+      "r"(lo), "r"(hi)
+      : "memory");
 }
-__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ uint32_t cluster_ctarank() {
   uint32_t r;
@@ -129,32 +151,65 @@ __device__ __forceinline__ void st_cluster_f32(uint32_t saddr, uint32_t rank, fl
       : "memory");
 }
 
-__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, const Fp4GemmArgs& a,
-                                              volatile int* abort_flag) {
-  if (mbar_try_wait(bar, parity)) return true;
+// mbarrier.try_wait that may suspend the thread for up to kSuspendNs (it wakes when the phase
+// completes). With the default limit the dozen waiting warps poll shared memory hard enough to
+// slow the MMAs' own reads of it.
+constexpr uint32_t kSuspendNs = 1000000;
+__device__ __forceinline__ bool try_wait_suspend(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(kSuspendNs)
+      : "memory");
+  return ok != 0;
+}
+
+// The slow path of a wait, kept out of line: the roles' loops have to stay small (their warps share
+// the SM's instruction caches).
+__device__ __noinline__ bool wait_longer(uint64_t* bar, uint32_t parity, unsigned long long timeout_ns, int* status,
+                                         volatile int* abort_flag) {
   const uint64_t t0 = globaltimer_ns();
   while (true) {
-#pragma unroll 1
-    for (int i = 0; i < 32; ++i)
-      if (mbar_try_wait(bar, parity)) return true;
+    if (try_wait_suspend(bar, parity)) return true;
     if (*abort_flag) return false;
-    if (globaltimer_ns() - t0 > a.timeout_ns) {
+    if (globaltimer_ns() - t0 > timeout_ns) {
       *abort_flag = 1;
-      report_status(a.status, kStatusTimeout);
+      report_status(status, kStatusTimeout);
       return false;
     }
   }
 }
+__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, const Fp4GemmArgs& a,
+                                              volatile int* abort_flag) {
+  return try_wait_suspend(bar, parity) || wait_longer(bar, parity, a.timeout_ns, a.status, abort_flag);
+}
+// The same by a whole converged warp, which leaves it together: the loop branches on a vote alone and
+// calls nothing, so that the code around it keeps its addresses in uniform registers. Bounded by the
+// number of tries, each of which returns after kSuspendNs at the latest.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint32_t tries) {
+  for (uint32_t i = 0; !__all_sync(0xffffffffu, try_wait_suspend(bar, parity)); ++i)
+    if (i >= tries) return false;
+  return true;
+}
+
+// A value that is the same in all lanes, into a uniform register.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __reduce_or_sync(0xffffffffu, v); }
 
 struct Tile {
-  int g, m, row0, nrows;
+  int g;           // expert
+  int row0, rows;  // tokens
+  int col0, cols;  // rows of w[g]
+  int xtile, wtile;  // number of the token tile and of the w tile
 };
 
 // Tile t: experts in order, inside an expert the w tiles in order, inside a w tile its token
 // tiles, so that CTAs taking consecutive tiles read the same weights together, through L2.
 // `pre` holds each expert's first token tile, `row` its first row.
-template <int kBN>
-__device__ __forceinline__ Tile tile_of(int t, int E, int m_tiles, const int* pre, const int* row) {
+template <int kTokens, int kCols>
+__device__ __noinline__ Tile tile_of_(int t, int E, int N, int m_tiles, const int* pre, const int* row) {
   int lo = 0, hi = E - 1;
   const int want = t / m_tiles;  // pre[g] * m_tiles <= t  <=>  pre[g] <= t / m_tiles
   while (lo < hi) {
@@ -163,13 +218,55 @@ __device__ __forceinline__ Tile tile_of(int t, int E, int m_tiles, const int* pr
   }
   const int nt = pre[lo + 1] - pre[lo];
   const int local = t - pre[lo] * m_tiles;
+  const int m = local / nt, n = local - m * nt;
   Tile r;
   r.g = lo;
-  r.m = local / nt;
-  const int n = local % nt;
-  r.row0 = row[lo] + n * kBN;
-  r.nrows = min(kBN, row[lo + 1] - r.row0);
+  r.row0 = row[lo] + n * kTokens;
+  r.rows = min(kTokens, row[lo + 1] - r.row0);
+  r.col0 = m * kCols;
+  r.cols = min(kCols, N - r.col0);
+  r.xtile = pre[lo] + n;
+  r.wtile = lo * m_tiles + m;
   return r;
+}
+template <class C>
+__device__ __forceinline__ Tile tile_of(int t, const Fp4GemmArgs& a, const int* pre, const int* row) {
+  return tile_of_<C::kTokens, C::kCols>(t, a.E, a.N, a.m_tiles, pre, row);
+}
+
+// The experts' rows and token tiles, by one warp, 32 experts at a time: row[g] the first row of expert
+// g (clamped to [0, T] and to ascending order), pre[g] its first token tile, g = 0 .. E.
+template <int kTokens>
+__device__ __forceinline__ void scan_experts(const int32_t* offsets, int E, int T, int* pre, int* row) {
+  const int lane = threadIdx.x % 32;
+  int last = 0, tiles = 0;
+  for (int b = 0; b <= E; b += 32) {
+    const int g = b + lane;
+    int v = 0;
+    if (g <= E) v = offsets ? max(0, min(T, __ldg(offsets + g))) : (g == 0 ? 0 : T);
+    // running maximum: offsets that go back leave an expert without rows
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v = max(v, u);
+    }
+    v = max(v, last);
+    int before = __shfl_up_sync(0xffffffffu, v, 1);
+    if (lane == 0) before = last;
+    // token tiles of expert g - 1 end at g
+    int n = g > 0 && g <= E ? (v - before + kTokens - 1) / kTokens : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, n, o);
+      if (lane >= o) n += u;
+    }
+    if (g <= E) {
+      row[g] = v;
+      pre[g] = tiles + n;
+    }
+    tiles += __shfl_sync(0xffffffffu, n, 31);
+    last = __shfl_sync(0xffffffffu, v, 31);
+  }
 }
 
 // kBytes (8 or 16) to shared memory, the first n of them from global memory, zeros behind.
@@ -200,48 +297,78 @@ __device__ __forceinline__ void read_scales(const uint8_t* p, uint32_t* w) {
   }
 }
 
-template <typename T>
-__device__ __forceinline__ T round_out(float v);
-template <>
-__device__ __forceinline__ float round_out<float>(float v) {
-  return v;
-}
-template <>
-__device__ __forceinline__ __nv_bfloat16 round_out<__nv_bfloat16>(float v) {
-  return __float2bfloat16_rn(v);
-}
-template <>
-__device__ __forceinline__ __half round_out<__half>(float v) {
-  return __float2half_rn(v);
-}
-
-// 16 columns (tokens) of one output row n = m of w: lanes hold consecutive n.
-template <typename T>
-__device__ __forceinline__ void store_chunk(void* out, int64_t ld, int row0, int c0, int nrows, int n, bool n_ok,
-                                            float alpha, const uint32_t (&r)[16]) {
-  if (!n_ok) return;
-  T* p = static_cast<T*>(out) + static_cast<int64_t>(row0 + c0) * ld + n;
-#pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    if (c0 + j < nrows) *p = round_out<T>(alpha * __uint_as_float(r[j]));
-    p += ld;
+__device__ __forceinline__ uint32_t pack_pair(bool bf, float lo, float hi) {
+  if (bf) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
   }
-}
-__device__ __forceinline__ void store_any(const Fp4GemmArgs& a, int row0, int c0, int nrows, int n, bool n_ok,
-                                          float alpha, const uint32_t (&r)[16]) {
-  if (a.out_dtype == kValBf16)
-    store_chunk<__nv_bfloat16>(a.out, a.N, row0, c0, nrows, n, n_ok, alpha, r);
-  else if (a.out_dtype == kValFp16)
-    store_chunk<__half>(a.out, a.N, row0, c0, nrows, n, n_ok, alpha, r);
-  else
-    store_chunk<float>(a.out, a.N, row0, c0, nrows, n, n_ok, alpha, r);
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-template <bool kNv, int kHalves, int kBN, bool kSplit>
+// 16 tokens of output column n = this lane's row of w, as 16-bit pairs (token 2j low, 2j + 1 high).
+// vec: four lanes exchange theirs so that each holds four consecutive columns of a token, and a warp
+// stores 64 bytes of four tokens at a time instead of 64 bytes of one (8 shuffles and 4 stores for
+// 16 stores); N % 4 == 0 keeps a group of four on one side of N.
+__device__ __forceinline__ void store_pairs(const Fp4GemmArgs& a, int row0, int c0, int nrows, int n, int lane,
+                                            bool vec, const uint32_t (&p)[8]) {
+  uint16_t* out = static_cast<uint16_t*>(a.out) + static_cast<int64_t>(row0 + c0) * a.N;
+  if (vec) {
+    const bool odd = lane & 1, up = lane & 2;
+    uint32_t q[8];  // q[m]: token 2m + odd, columns n & ~1 and the next
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t lo = __byte_perm(p[2 * i], p[2 * i + 1], 0x5410), hi = __byte_perm(p[2 * i], p[2 * i + 1], 0x7632);
+      const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? lo : hi, 1);
+      const uint32_t l = odd ? got : lo, r = odd ? hi : got;
+      q[2 * i] = __byte_perm(l, r, 0x5410);
+      q[2 * i + 1] = __byte_perm(l, r, 0x7632);
+    }
+    const int token = lane & 3;
+    uint16_t* dst = out + static_cast<int64_t>(token) * a.N + (n & ~3);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t keep = up ? q[2 * i + 1] : q[2 * i];
+      const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? q[2 * i] : q[2 * i + 1], 2);
+      if (n < a.N && c0 + 4 * i + token < nrows)
+        *reinterpret_cast<uint2*>(dst) = up ? make_uint2(got, keep) : make_uint2(keep, got);
+      dst += 4 * static_cast<int64_t>(a.N);
+    }
+    return;
+  }
+  if (n >= a.N) return;
+#pragma unroll
+  for (int j = 0; j < 16; ++j)
+    if (c0 + j < nrows)
+      out[static_cast<int64_t>(j) * a.N + n] = static_cast<uint16_t>(p[j / 2] >> (16 * (j & 1)));
+}
+
+// 16 accumulator columns (tokens) c0 .. c0 + 15 of row m of the tile, scaled and stored.
+__device__ __forceinline__ void store_16(const Fp4GemmArgs& a, const Tile& tl, int m, int c0, int lane, bool vec,
+                                         float alpha, const uint32_t (&r)[16]) {
+  if (a.out_dtype == kValFp32) {
+    float* p = static_cast<float*>(a.out) + static_cast<int64_t>(tl.row0 + c0) * a.N + tl.col0 + m;
+    if (m < tl.cols) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        if (c0 + j < tl.rows) *p = alpha * __uint_as_float(r[j]);
+        p += a.N;
+      }
+    }
+    return;
+  }
+  const bool bf = a.out_dtype == kValBf16;
+  uint32_t v[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = pack_pair(bf, alpha * __uint_as_float(r[2 * j]), alpha * __uint_as_float(r[2 * j + 1]));
+  store_pairs(a, tl.row0, c0, tl.rows, tl.col0 + m, lane, vec, v);
+}
+
+template <bool kNv, bool kPre, int kHalves, int kBN, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
-    gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+    gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                     const Fp4GemmArgs args) {
-  using C = Cfg<kNv, kHalves, kBN>;
+  using C = Cfg<kNv, kPre, kHalves, kBN>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sA = smem;
@@ -250,12 +377,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(sRaw + C::kRaw * C::kRawBytes);
   uint64_t* full = bars;
   uint64_t* empty = full + C::kStages;
-  uint64_t* sffull = empty + C::kStages;
-  uint64_t* sfempty = sffull + C::kSets;
-  uint64_t* tfull = sfempty + C::kSets;
+  uint64_t* tfull = empty + C::kStages;
   uint64_t* tempty = tfull + C::kAccs;
-  uint64_t* rfull = tempty + C::kAccs;
-  uint64_t* rempty = rfull + C::kRaw;
+  uint64_t* rfull = tempty + C::kAccs;   // scale rows landed
+  uint64_t* rturned = rfull + C::kRaw;   // ... and put in the MMA's order
+  uint64_t* rempty = rturned + C::kRaw;
   uint64_t* drain = rempty + C::kRaw;
   uint32_t* tmem_base_smem = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_base_smem + 1);
@@ -270,64 +396,33 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
     }
-    for (int i = 0; i < C::kSets; ++i) {
-      mbar_init(&sffull[i], kSfWarps);
-      mbar_init(&sfempty[i], 1);
+    for (int i = 0; i < C::kRaw; ++i) {
+      mbar_init(&rfull[i], 32);
+      mbar_init(&rturned[i], kSfWarps);
+      mbar_init(&rempty[i], 1);
     }
     for (int i = 0; i < C::kAccs; ++i) {
       mbar_init(&tfull[i], 1);
-      mbar_init(&tempty[i], kEpiWarps);
-    }
-    for (int i = 0; i < C::kRaw; ++i) {
-      mbar_init(&rfull[i], 32);
-      mbar_init(&rempty[i], kSfWarps);
+      mbar_init(&tempty[i], C::kEpiWarps);
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbarrier_init();
-    tma_prefetch_desc(&tmW);
-    tma_prefetch_desc(&tmX);
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
   }
   if (warp == 1) {
     tmem_alloc(tmem_base_smem, 512);
     tmem_relinquish();
   }
-  // the experts' rows and token tiles: warp 2 scans 32 experts at a time
-  if (warp == kFirstSf) {
-    int last = 0, tiles = 0;
-    for (int b = 0; b <= args.E; b += 32) {
-      const int g = b + lane;
-      int v = 0;
-      if (g <= args.E) v = args.offsets ? max(0, min(args.T, __ldg(args.offsets + g))) : (g == 0 ? 0 : args.T);
-      // running maximum: offsets that go back leave an expert without rows
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v = max(v, u);
-      }
-      v = max(v, last);
-      int before = __shfl_up_sync(0xffffffffu, v, 1);
-      if (lane == 0) before = last;
-      // token tiles of expert g - 1 end at g
-      int n = g > 0 && g <= args.E ? (v - before + kBN - 1) / kBN : 0;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, n, o);
-        if (lane >= o) n += u;
-      }
-      if (g <= args.E) {
-        row_s[g] = v;
-        pre[g] = tiles + n;
-      }
-      tiles += __shfl_sync(0xffffffffu, n, 31);
-      last = __shfl_sync(0xffffffffu, v, 31);
-    }
-  }
+  if (warp == kFirstSf) scan_experts<C::kTokens>(args.offsets, args.E, args.T, pre, row_s);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_base_smem;
-  const int total = pre[args.E] * args.m_tiles;
+  // a loop bound that came from memory would make the compiler treat the MMA warp's loop as divergent:
+  // each tcgen05 instruction then costs some 35 cycles of moves into uniform registers instead of 8
+  const int total = static_cast<int>(uniform(static_cast<uint32_t>(pre[args.E] * args.m_tiles)));
 
   // split: one tile per cluster, K cut into `splits` slices; otherwise a strided list of tiles
   const int rank = kSplit ? static_cast<int>(cluster_ctarank()) : 0;
@@ -344,20 +439,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t phase = 0;
       long issued = 0;
       for (int t = t0; t < total && !*abort_flag; t += stride) {
-        const Tile tl = tile_of<kBN>(t, args.E, args.m_tiles, pre, row_s);
-        const int w_row = tl.g * args.N + tl.m * 128 * kHalves;
-        const int nb = (tl.nrows + kBox - 1) / kBox;
+        const Tile tl = tile_of<C>(t, args, pre, row_s);
+        const int w_row = tl.g * args.N + tl.col0;
+        const int nb = (tl.rows + kBox - 1) / kBox;
+        // weights that one token tile alone reads stream past; what many tiles read stays in L2
+        constexpr uint64_t w_hint = kBN >= 192 ? kCacheEvictNormal : kCacheEvictFirst;
         bool ok = true;
         for (int kb = kb0; kb < kb1; ++kb) {
           if (!wait_or_abort(&empty[stage], phase ^ 1, args, abort_flag)) {
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(&full[stage], C::kABytes + nb * kBox * kRowBytes);
-          tma_load_2d(sA + stage * C::kABytes, &tmW, &full[stage], kb * kRowBytes, w_row, kCacheEvictFirst);
+          mbar_arrive_expect_tx(&full[stage], C::kABytes + nb * kBox * kRowBytes + (kPre ? C::kRawBytes : 0));
+          tma_load_2d(sA + stage * C::kABytes, &tmA, &full[stage], kb * kRowBytes, w_row, w_hint);
           for (int j = 0; j < nb; ++j)
-            tma_load_2d(sB + stage * C::kBBytes + j * kBox * kRowBytes, &tmX, &full[stage], kb * kRowBytes,
+            tma_load_2d(sB + stage * C::kBBytes + j * kBox * kRowBytes, &tmB, &full[stage], kb * kRowBytes,
                         tl.row0 + j * kBox, kCacheEvictLast);
+          if constexpr (kPre) {
+            const int64_t wt = static_cast<int64_t>(tl.wtile) * args.num_kb + kb;
+            const int64_t xt = static_cast<int64_t>(tl.xtile) * args.num_kb + kb;
+            uint8_t* sf = sRaw + stage * C::kRawBytes;
+            bulk_load(sf, args.ws_tiles + wt * C::kASfBytes, C::kASfBytes, &full[stage], kCacheEvictNormal);
+            bulk_load(sf + C::kASfBytes, args.xs_tiles + xt * C::kBSfBytes, C::kBSfBytes, &full[stage],
+                      kCacheEvictNormal);
+          }
           ++issued;
           if (++stage == C::kStages) {
             stage = 0;
@@ -378,128 +483,199 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      int stage = 0, set = 0, acc = 0;
-      uint32_t phase = 0, sphase = 0, aphase = 0;
-      for (int t = t0; t < total && !*abort_flag; t += stride) {
-        const Tile tl = tile_of<kBN>(t, args.E, args.m_tiles, pre, row_s);
-        const uint32_t n_mma = (tl.nrows + 15) & ~15;
-        if (!wait_or_abort(&tempty[acc], aphase ^ 1, args, abort_flag)) break;
-        tc_fence_after();
-        const uint32_t d = tmem_base + acc * C::kAccCols;
-        bool ok = true;
-        for (int kb = kb0; kb < kb1; ++kb) {
-          if (!wait_or_abort(&full[stage], phase, args, abort_flag) ||
-              !wait_or_abort(&sffull[set], sphase, args, abort_flag)) {
-            ok = false;
-            break;
+    // The whole warp walks the stages and agrees on every wait, so that the loop and its addresses
+    // are the same in all lanes (uniform registers); one elected lane issues. With the loop inside
+    // `lane == 0` a tcgen05 instruction took some 80 cycles to issue, with waits that each lane
+    // judged by itself 57.
+    //
+    // kPre: the copies of the next stage's scales go ahead of a stage's last MMAs. Copies issued ahead of
+    // a stage's own first MMAs leave the tensor core idle, and the columns they go to are free only
+    // once the stage before this one is through.
+    const bool elected = elect_one();
+    const uint32_t tmem = uniform(tmem_base);
+    const uint32_t tries = static_cast<uint32_t>(args.timeout_ns / kSuspendNs);
+    const uint64_t tile_desc = sdesc_sw128(smem_u32(sA)), raw_desc = sdesc_plain(smem_u32(sRaw));
+    const uint32_t a_lo0 = static_cast<uint32_t>(tile_desc), hi = static_cast<uint32_t>(tile_desc >> 32);
+    const uint32_t b_lo0 = static_cast<uint32_t>(sdesc_sw128(smem_u32(sB)));
+    const uint32_t raw_lo0 = static_cast<uint32_t>(raw_desc), raw_hi = static_cast<uint32_t>(raw_desc >> 32);
+    int stage = 0, raw = 0, set = 0, acc = 0;
+    uint32_t phase = 0, rphase = 0, aphase = 0;
+    int old = 0;       // scale slot of the stage that used the next set of TMEM columns before
+    uint32_t ophase = 0;
+    int n_stage = 1;   // stages whose scales were copied so far, up to kSets
+    // blocks [b0, b1) of the scales in slot ra, to the columns of set se
+    auto copy_scales = [&](int ra, int se, int b0, int b1) {
+      const uint32_t sf = tmem + C::kSfBase + se * C::kSfCols;
+      const uint32_t lo = raw_lo0 + static_cast<uint32_t>(ra * (C::kRawBytes / 16));
+#pragma unroll
+      for (int b = 0; b < C::kBlocks; ++b)
+        if (b >= b0 && b < b1)
+#pragma unroll
+          for (int j = 0; j < C::kAtoms; ++j)
+            copy_word(sf + (b < kHalves ? (b * C::kAtoms + j) * 4
+                                        : kHalves * C::kAtoms * 4 + j * C::kBCols + (b - kHalves) * 4),
+                      lo + (b * C::kBlockBytes + j * 512) / 16, raw_hi);
+    };
+    bool ok = true;
+    if (kPre && t0 < total) {
+      ok = warp_wait(&full[0], 0, tries);
+      tc_fence_after();
+      if (elected) copy_scales(0, 0, 0, C::kBlocks);
+      __syncwarp();
+    }
+    // waits until the MMAs that last read the next set of TMEM columns are done: their scales' slot
+    // is free then (kSets <= kRaw: its barrier cannot have moved on by a second phase)
+    auto set_free = [&]() {
+      uint64_t* slot = kPre ? empty : rempty;
+      if (n_stage < C::kSets) {
+        ++n_stage;
+        return true;
+      }
+      const bool w = warp_wait(&slot[old], ophase, tries);
+      if (++old == C::kRaw) {
+        old = 0;
+        ophase ^= 1;
+      }
+      return w;
+    };
+    for (int t = t0; ok && t < total; t += stride) {
+      const Tile tl = tile_of<C>(t, args, pre, row_s);
+      const uint32_t n_mma = (tl.rows + 15) & ~15;
+      const uint32_t idesc = uniform(idesc_fp4(kNv, n_mma));
+      ok = warp_wait(&tempty[acc], aphase ^ 1, tries);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t d = tmem + acc * C::kAccCols;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        const uint32_t sf = tmem + C::kSfBase + set * C::kSfCols;
+        const uint32_t a_lo = a_lo0 + static_cast<uint32_t>(stage * (C::kABytes / 16));
+        const uint32_t b_lo = b_lo0 + static_cast<uint32_t>(stage * (C::kBBytes / 16));
+        const uint32_t first = kb != kb0;
+        auto mma_step = [&](uint32_t j, uint32_t accumulate) {
+          const uint32_t atom = kNv ? j : j / 2, id = kNv ? 0 : (j & 1) * 2;
+#pragma unroll
+          for (uint32_t h = 0; h < kHalves; ++h)
+            umma_fp4<kNv>(d + h * kBN, a_lo + (h * 128 * kRowBytes + j * 32) / 16, b_lo + j * 2, hi,
+                          idesc | (id << 4) | (id << 29), (sf + (h * C::kAtoms + atom) * 4) | (id << 30),
+                          (sf + kHalves * C::kAtoms * 4 + atom * C::kBCols) | (id << 30), accumulate);
+        };
+        if constexpr (kPre) {
+          // this stage arrived with the last one's wait
+          if (elected) {
+            mma_step(0, first);
+            mma_step(1, 1u);
+            mma_step(2, 1u);
           }
+          __syncwarp();
+          const int nstage = stage + 1 == C::kStages ? 0 : stage + 1;
+          const uint32_t nphase = stage + 1 == C::kStages ? phase ^ 1 : phase;
+          const int nset = set + 1 == C::kSets ? 0 : set + 1;
+          if (kb + 1 < kb1 || t + stride < total) {
+            ok = warp_wait(&full[nstage], nphase, tries) && set_free();
+            if (!ok) break;
+            tc_fence_after();
+          }
+          // no branch in here: behind the last stage of all, the copies bring what nothing reads
+          // (with the copies under a condition the compiler gave up the uniform registers of the whole
+          // region, and a stage took 1510 cycles instead of 920)
+          if (elected) {
+            copy_scales(nstage, nset, 0, C::kBlocks);
+            mma_step(3, 1u);
+            umma_commit(&empty[stage]);
+          }
+          __syncwarp();
+          stage = nstage;
+          phase = nphase;
+          set = nset;
+        } else {
+          ok = warp_wait(&rturned[raw], rphase, tries) && (kb == kb0 && t == t0 ? true : set_free()) &&
+               warp_wait(&full[stage], phase, tries);
+          if (!ok) break;
           tc_fence_after();
-          const uint32_t a_addr = smem_u32(sA + stage * C::kABytes);
-          const uint32_t b_addr = smem_u32(sB + stage * C::kBBytes);
-          const uint32_t sf = tmem_base + C::kSfBase + set * C::kSfCols;
-#pragma unroll
-          for (uint32_t j = 0; j < 4; ++j) {
-            const uint32_t atom = kNv ? j : j / 2, id = kNv ? 0 : (j & 1) * 2;
-            const uint32_t idesc = idesc_fp4(kNv, n_mma, id);
-            const uint64_t bdesc = sdesc_sw128(b_addr + j * 32);
-            const uint32_t sfb = (sf + kHalves * C::kAtoms * 4 + atom * C::kBCols) | (id << 30);
-#pragma unroll
-            for (uint32_t h = 0; h < kHalves; ++h)
-              umma_fp4<kNv>(d + h * kBN, sdesc_sw128(a_addr + h * 128 * kRowBytes + j * 32), bdesc, idesc,
-                            (sf + (h * C::kAtoms + atom) * 4) | (id << 30), sfb, kb != kb0 || j != 0);
+          if (elected) {
+            copy_scales(raw, set, 0, C::kBlocks);
+            mma_step(0, first);
+            mma_step(1, 1u);
+            mma_step(2, 1u);
+            mma_step(3, 1u);
+            umma_commit(&empty[stage]);
+            umma_commit(&rempty[raw]);
           }
-          umma_commit(&empty[stage]);
-          umma_commit(&sfempty[set]);
+          __syncwarp();
           if (++stage == C::kStages) {
             stage = 0;
             phase ^= 1;
           }
-          if (++set == C::kSets) {
-            set = 0;
-            sphase ^= 1;
+          if (++raw == C::kRaw) {
+            raw = 0;
+            rphase ^= 1;
           }
-        }
-        if (!ok) break;
-        umma_commit(&tfull[acc]);
-        if (++acc == C::kAccs) {
-          acc = 0;
-          aphase ^= 1;
+          if (++set == C::kSets) set = 0;
         }
       }
-      // every MMA done before TMEM and shared memory go
+      if (!ok) break;
+      if (elected) umma_commit(&tfull[acc]);
+      __syncwarp();
+      if (++acc == C::kAccs) {
+        acc = 0;
+        aphase ^= 1;
+      }
+    }
+    if (!ok && elected) {
+      *abort_flag = 1;
+      report_status(args.status, kStatusTimeout);
+    }
+    // every MMA done before TMEM and shared memory go
+    if (elected) {
       umma_commit(drain);
       const uint64_t b = globaltimer_ns();
       while (!mbar_try_wait(drain, 0) && globaltimer_ns() - b < args.timeout_ns) {
       }
     }
-  } else if (warp < kFirstEpi) {
-    // ------------------------------------------------------------ scale factors -> TMEM
+    __syncwarp();
+  } else if (!kPre && warp < C::kFirstEpi) {
+    // ------------------------------------------------------------ scale rows -> the MMA's order
     constexpr int kW = C::kAtoms;
-    constexpr int kARows = 4 * kHalves, kBRows = kBN / 32;  // rows of this lane: 32 apart
-    const uint32_t quarter = tmem_base + (static_cast<uint32_t>((warp & 3) * 32) << 16) + C::kSfBase;
-    int set = 0, raw = 0;
-    uint32_t sphase = 0, rphase = 0;
+    int raw = 0;
+    uint32_t rphase = 0;
     bool ok = true;
     for (int t = t0; ok && t < total; t += stride) {
       for (int kb = kb0; kb < kb1; ++kb) {
-        if (lane == 0)
-          ok = wait_or_abort(&rfull[raw], rphase, args, abort_flag) &&
-               wait_or_abort(&sfempty[set], sphase ^ 1, args, abort_flag);
+        if (lane == 0) ok = wait_or_abort(&rfull[raw], rphase, args, abort_flag);
         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
         if (!ok) break;
-        tc_fence_after();
-        const uint8_t* src = sRaw + raw * C::kRawBytes + lane * C::kRowSf;
-        const uint32_t base = quarter + set * C::kSfCols;
-#pragma unroll
-        for (int h = 0; h < kHalves; ++h) {
+        for (int b = warp - kFirstSf; b < C::kBlocks; b += kSfWarps) {
+          uint8_t* block = sRaw + raw * C::kRawBytes + b * C::kBlockBytes;
           uint32_t w[4 * kW];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) read_scales<kW>(src + (4 * h + i) * 32 * C::kRowSf, w + i * kW);
-#pragma unroll
-          for (int j = 0; j < kW; ++j) tmem_st4(base + (h * kW + j) * 4, w[j], w[kW + j], w[2 * kW + j], w[3 * kW + j]);
-        }
-#pragma unroll
-        for (int c = 0; c < C::kBCols; c += 4) {
-          uint32_t w[4 * kW];
-#pragma unroll
-          for (int i = 0; i < 4 * kW; ++i) w[i] = 0u;
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (c + i < kBRows) read_scales<kW>(src + (kARows + c + i) * 32 * C::kRowSf, w + i * kW);
+          for (int i = 0; i < 4; ++i) read_scales<kW>(block + (32 * i + lane) * C::kRowSf, w + i * kW);
+          __syncwarp();  // every row is read before any column is written
 #pragma unroll
           for (int j = 0; j < kW; ++j)
-            tmem_st4(base + kHalves * kW * 4 + j * C::kBCols + c, w[j], w[kW + j], w[2 * kW + j], w[3 * kW + j]);
+            *reinterpret_cast<uint4*>(block + j * 512 + lane * 16) =
+                make_uint4(w[j], w[kW + j], w[2 * kW + j], w[3 * kW + j]);
         }
-        tmem_st_wait();
-        tc_fence_before();
+        fence_proxy_async_smem();  // the tensor core reads what these generic stores wrote
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&rempty[raw]);
-          mbar_arrive(&sffull[set]);
-        }
-        if (++set == C::kSets) {
-          set = 0;
-          sphase ^= 1;
-        }
+        if (lane == 0) mbar_arrive(&rturned[raw]);
         if (++raw == C::kRaw) {
           raw = 0;
           rphase ^= 1;
         }
       }
     }
-  } else if (warp == kSfLoader) {
+  } else if (!kPre && warp == kSfLoader) {
     // ------------------------------------------------------------ scale rows -> shared memory
     constexpr int kB = C::kRowSf;
     int raw = 0;
     uint32_t rphase = 0;
     bool ok = true;
+    const int64_t w_step = 32 * args.ws_stride, x_step = 32 * args.xs_stride;
     for (int t = t0; ok && t < total; t += stride) {
-      const Tile tl = tile_of<kBN>(t, args.E, args.m_tiles, pre, row_s);
-      const int n = tl.m * 128 * kHalves + lane;
-      const int w_left = args.N - n, x_left = tl.nrows - lane;  // rows from this lane's first one
-      const uint8_t* wrow = args.ws + (static_cast<int64_t>(tl.g) * args.N + n) * args.ws_stride;
+      const Tile tl = tile_of<C>(t, args, pre, row_s);
+      const uint8_t* wrow = args.ws + (static_cast<int64_t>(tl.g) * args.N + tl.col0 + lane) * args.ws_stride;
       const uint8_t* xrow = args.xs + static_cast<int64_t>(tl.row0 + lane) * args.xs_stride;
+      const int w_left = tl.cols - lane, x_left = tl.rows - lane;  // rows from this lane's first one
       for (int kb = kb0; kb < kb1; ++kb) {
         if (lane == 0) ok = wait_or_abort(&rempty[raw], rphase ^ 1, args, abort_flag);
         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
@@ -507,18 +683,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t dst = smem_u32(sRaw + raw * C::kRawBytes + lane * kB);
         const int off = kb * kB;
         const int left = min(kB, args.sf_cols - off);
+        const uint8_t* pw = wrow + off;
+        const uint8_t* px = xrow + off;
         // a row outside reads nothing (0 bytes from the scales' own start)
 #pragma unroll
         for (int i = 0; i < 4 * kHalves; ++i) {
           const bool in = 32 * i < w_left;
-          cp_async_zfill<kB>(dst + i * 32 * kB, in ? wrow + static_cast<int64_t>(i) * 32 * args.ws_stride + off : args.ws,
-                             in ? left : 0);
+          cp_async_zfill<kB>(dst + i * 32 * kB, in ? pw : args.ws, in ? left : 0);
+          pw += w_step;
         }
 #pragma unroll
         for (int i = 0; i < kBN / 32; ++i) {
           const bool in = 32 * i < x_left;
-          cp_async_zfill<kB>(dst + (4 * kHalves + i) * 32 * kB,
-                             in ? xrow + static_cast<int64_t>(i) * 32 * args.xs_stride + off : args.xs, in ? left : 0);
+          cp_async_zfill<kB>(dst + (4 * kHalves + i) * 32 * kB, in ? px : args.ws, in ? left : 0);
+          px += x_step;
         }
         cp_async_arrive(&rfull[raw]);
         if (++raw == C::kRaw) {
@@ -529,15 +707,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // copies in flight land before the CTA's shared memory goes
     asm volatile("cp.async.wait_all;" ::: "memory");
-  } else {
+  } else if (warp >= C::kFirstEpi && warp < kSfLoader) {
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;
-    const int cfirst = ((warp - kFirstEpi) / 4) * 16;
+    const int cfirst = ((warp - C::kFirstEpi) / 4) * 16;
     const float xts = args.x_ts ? __ldg(args.x_ts) : 1.0f;
+    const bool vec_out = args.N % 4 == 0 && (reinterpret_cast<uintptr_t>(args.out) & 7) == 0;
     int acc = 0;
     uint32_t aphase = 0;
     for (int t = t0; t < total; t += stride) {
-      const Tile tl = tile_of<kBN>(t, args.E, args.m_tiles, pre, row_s);
+      const Tile tl = tile_of<C>(t, args, pre, row_s);
       bool ok = true;
       if (lane == 0) ok = wait_or_abort(&tfull[acc], aphase, args, abort_flag);
       ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
@@ -546,14 +725,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       if constexpr (!kSplit) {
         const float alpha = args.w_ts ? xts * __ldg(args.w_ts + tl.g) : xts;
         const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * C::kAccCols;
-        const int n = tl.m * 128 * kHalves + q * 32 + lane;
-        for (int c0 = cfirst; c0 < tl.nrows; c0 += 16 * kEpiGroups) {
-#pragma unroll
+        const int mine = q * 32 + lane;  // this lane's row of the tile's first half
+#pragma unroll 1
+        for (int c0 = cfirst; c0 < tl.rows; c0 += 16 * C::kEpiGroups) {
+#pragma unroll 1
           for (int h = 0; h < kHalves; ++h) {
             uint32_t r[16];
             tmem_ld16(tb + h * kBN + c0, r);
             tmem_ld_wait();
-            store_any(args, tl.row0, c0, tl.nrows, n + h * 128, n + h * 128 < args.N, alpha, r);
+            store_16(args, tl, mine + h * 128, c0, lane, vec_out, alpha, r);
           }
         }
         tc_fence_before();
@@ -573,12 +753,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     cluster_sync_all();
     const int q = warp & 3;
-    const int cfirst = ((warp - kFirstEpi) / 4) * 16;
-    const bool work = warp >= kFirstEpi && warp < kSfLoader && t0 < total && !*abort_flag;
+    const int cfirst = ((warp - C::kFirstEpi) / 4) * 16;
+    const bool work = warp >= C::kFirstEpi && warp < kSfLoader && t0 < total && !*abort_flag;
     Tile tl{};
-    if (work) tl = tile_of<kBN>(t0, args.E, args.m_tiles, pre, row_s);
+    if (work) tl = tile_of<C>(t0, args, pre, row_s);
     uint32_t r[16];
-    if (work && cfirst < tl.nrows) {
+    if (work && cfirst < tl.rows) {
       tc_fence_after();
       tmem_ld16(tmem_base + (static_cast<uint32_t>(q * 32) << 16) + cfirst, r);
       tmem_ld_wait();
@@ -590,7 +770,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
     cluster_sync_all();
-    if (work && rank == 0 && cfirst < tl.nrows) {
+    if (work && rank == 0 && cfirst < tl.rows) {
       const float* part = reinterpret_cast<const float*>(sA) + cfirst * 128 + q * 32 + lane;
       for (int p = 0; p < splits - 1; ++p)
 #pragma unroll
@@ -598,8 +778,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           r[j] = __float_as_uint(__uint_as_float(r[j]) + part[(p * kBN + j) * 128]);
       const float xts = args.x_ts ? __ldg(args.x_ts) : 1.0f;
       const float alpha = args.w_ts ? xts * __ldg(args.w_ts + tl.g) : xts;
-      const int n = tl.m * 128 + q * 32 + lane;
-      store_any(args, tl.row0, cfirst, tl.nrows, n, n < args.N, alpha, r);
+      const int m = q * 32 + lane;
+      const bool vec_out = args.N % 4 == 0 && (reinterpret_cast<uintptr_t>(args.out) & 7) == 0;
+      store_16(args, tl, m, cfirst, lane, vec_out, alpha, r);
     }
   }
   tc_fence_before();
@@ -610,12 +791,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <bool kNv, int kHalves, int kBN, bool kSplit>
+template <bool kNv, bool kPre, int kHalves, int kBN, bool kSplit>
 cudaError_t launch_cfg(const CUtensorMap& tw, const CUtensorMap& tx, const Fp4GemmArgs& a, int grid, cudaStream_t s) {
-  using C = Cfg<kNv, kHalves, kBN>;
-  auto* kernel = gemm_fp4_kernel<kNv, kHalves, kBN, kSplit>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+  using C = Cfg<kNv, kPre, kHalves, kBN>;
+  auto* kernel = gemm_fp4_kernel<kNv, kPre, kHalves, kBN, kSplit>;
+  // the kernel's shared memory, allowed once per device
+  static std::atomic<uint64_t> allowed{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  if (dev >= 64 || !((allowed.load(std::memory_order_relaxed) >> dev) & 1)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) allowed.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
+  }
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(kThreads);
@@ -630,48 +819,170 @@ cudaError_t launch_cfg(const CUtensorMap& tw, const CUtensorMap& tx, const Fp4Ge
   return cudaLaunchKernelEx(&cfg, kernel, tw, tx, a);
 }
 
+// Scales into the MMA's order: for each tile (of kCols rows of w, or of kTokens rows of x) and each K
+// block of 256, 128-row blocks of kNv ? 4 : 2 words, each word 512 bytes with row r at 16 (r % 32) +
+// 4 (r / 32); zeros for rows outside the tile and behind a row's end. Blocks x: the tiles of w, expert
+// by expert, then those of x; y: four K blocks each. A thread writes 16 bytes.
+template <bool kNv, int kRows>
+__device__ __forceinline__ void arrange_tile(const uint8_t* src, int64_t stride, int rows, int sf_cols, int num_kb,
+                                             uint4* out) {
+  constexpr int kWords = kNv ? 4 : 2, kBlocks = (kRows + 127) / 128, kSf = kNv ? 16 : 8;
+  constexpr int kPerKb = kBlocks * kWords * 32;  // 16-byte pieces of a K block
+  const bool words = (reinterpret_cast<uintptr_t>(src) | stride) % 4 == 0;
+  const int kb0 = blockIdx.y * 4, n = min(4, num_kb - kb0) * kPerKb;
+  for (int i = threadIdx.x; i < n; i += blockDim.x) {
+    const int kb = kb0 + i / kPerKb, p = i % kPerKb;
+    // neighbouring threads take a row's words, so that a row's bytes are read together
+    const int j = p % kWords, l = p / kWords % 32, b = p / (kWords * 32);
+    const int c = kb * kSf + j * 4;
+    uint32_t w[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int r = b * 128 + q * 32 + l;
+      w[q] = 0u;
+      if (r < rows && c < sf_cols) {
+        const uint8_t* s = src + static_cast<int64_t>(r) * stride + c;
+        if (words && c + 4 <= sf_cols) {
+          w[q] = __ldg(reinterpret_cast<const uint32_t*>(s));
+        } else {
+          for (int e = 0; e < 4; ++e)
+            if (c + e < sf_cols) w[q] |= static_cast<uint32_t>(__ldg(s + e)) << (8 * e);
+        }
+      }
+    }
+    out[static_cast<int64_t>(kb) * kPerKb + (b * kWords + j) * 32 + l] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+template <bool kNv, int kTokens, int kCols>
+__global__ void __launch_bounds__(256) arrange_scales_kernel(const Fp4GemmArgs a) {
+  constexpr int kWords = kNv ? 4 : 2;
+  __shared__ int pre[kMaxExperts + 1], row_s[kMaxExperts + 1];
+  if (threadIdx.x < 32) scan_experts<kTokens>(a.offsets, a.E, a.T, pre, row_s);
+  __syncthreads();
+  int tile = blockIdx.x;
+  if (tile < a.E * a.m_tiles) {
+    const int g = tile / a.m_tiles, m = tile - g * a.m_tiles;
+    if (row_s[g] == row_s[g + 1]) return;  // no row meets this expert
+    const int rows = min(kCols, a.N - m * kCols);
+    arrange_tile<kNv, kCols>(a.ws + (static_cast<int64_t>(g) * a.N + m * kCols) * a.ws_stride, a.ws_stride, rows,
+                             a.sf_cols, a.num_kb,
+                             reinterpret_cast<uint4*>(a.ws_tiles) +
+                                 static_cast<int64_t>(tile) * a.num_kb * ((kCols + 127) / 128 * kWords * 32));
+    return;
+  }
+  tile -= a.E * a.m_tiles;
+  if (tile >= pre[a.E]) return;
+  int lo = 0, hi = a.E - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (pre[mid] <= tile) lo = mid; else hi = mid - 1;
+  }
+  const int row0 = row_s[lo] + (tile - pre[lo]) * kTokens;
+  arrange_tile<kNv, kTokens>(a.xs + static_cast<int64_t>(row0) * a.xs_stride, a.xs_stride,
+                             min(kTokens, row_s[lo + 1] - row0), a.sf_cols, a.num_kb,
+                             reinterpret_cast<uint4*>(a.xs_tiles) +
+                                 static_cast<int64_t>(tile) * a.num_kb * ((kTokens + 127) / 128 * kWords * 32));
+}
+
+template <bool kNv, int kTokens, int kCols>
+cudaError_t launch_arrange(const Fp4GemmArgs& a, int64_t xtiles, cudaStream_t s) {
+  const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(a.E) * a.m_tiles + xtiles), (a.num_kb + 3) / 4);
+  arrange_scales_kernel<kNv, kTokens, kCols><<<grid, 256, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
 template <bool kNv>
 cudaError_t launch_fmt(const CUtensorMap& tw, const CUtensorMap& tx, const Fp4GemmArgs& a, const Fp4Plan& p,
                        int num_sms, cudaStream_t s) {
-  // token tiles: at most T / bn whole ones, and one partial one for each expert that has rows
-  const int64_t tok = a.E == 1 ? (a.T + p.bn - 1) / p.bn : a.T / p.bn + (a.E < a.T ? a.E : a.T);
-  const int64_t most = tok * a.m_tiles;
-  if (p.splits > 1)
-    return launch_cfg<kNv, 1, 32, true>(tw, tx, a, static_cast<int>(most) * p.splits, s);
+  const int64_t xtiles = a.E == 1 ? (a.T + p.tokens - 1) / p.tokens : a.T / p.tokens + (a.E < a.T ? a.E : a.T);
+  const int64_t most = xtiles * a.m_tiles;
+  if (p.tokens > 32) {
+    const cudaError_t e = p.tokens == 96 ? launch_arrange<kNv, 96, 256>(a, xtiles, s) : launch_arrange<kNv, 192, 256>(a, xtiles, s);
+    if (e != cudaSuccess) return e;
+  }
+  if (p.splits > 1) return launch_cfg<kNv, false, 1, 32, true>(tw, tx, a, static_cast<int>(most) * p.splits, s);
   const int grid = static_cast<int>(most < num_sms ? most : num_sms);
-  if (p.halves == 1) return launch_cfg<kNv, 1, 32, false>(tw, tx, a, grid, s);
-  if (p.bn == 32) return launch_cfg<kNv, 2, 32, false>(tw, tx, a, grid, s);
-  if (p.bn == 96) return launch_cfg<kNv, 2, 96, false>(tw, tx, a, grid, s);
-  return launch_cfg<kNv, 2, 192, false>(tw, tx, a, grid, s);
+  if (p.cols == 128) return launch_cfg<kNv, false, 1, 32, false>(tw, tx, a, grid, s);
+  if (p.tokens == 32) return launch_cfg<kNv, false, 2, 32, false>(tw, tx, a, grid, s);
+  if (p.tokens == 96) return launch_cfg<kNv, true, 2, 96, false>(tw, tx, a, grid, s);
+  return launch_cfg<kNv, true, 2, 192, false>(tw, tx, a, grid, s);
 }
 
 }  // namespace
 
+// Bytes of one tile's arranged scales of one K block.
+static int64_t tile_sf_bytes(int format, int rows) { return (rows + 127) / 128 * (format == kFp4Nv ? 4 : 2) * 512; }
+static int64_t token_tiles(int T, int E, int tokens) {
+  // at most T / tokens whole ones, and one partial one for each expert that has rows
+  return E == 1 ? (T + tokens - 1) / tokens : T / tokens + (E < T ? E : T);
+}
+
+int64_t fp4_workspace(int format, int T, int N, int E, int num_kb, const Fp4Plan& p) {
+  if (p.tokens == 32) return 0;
+  const int64_t wt = static_cast<int64_t>(E) * ((N + p.cols - 1) / p.cols);
+  return num_kb * (wt * tile_sf_bytes(format, p.cols) + token_tiles(T, E, p.tokens) * tile_sf_bytes(format, p.tokens));
+}
+
 // Tile shape. Up to 32 rows per expert (on average, where there are several) a tile is 32 tokens
 // wide; its height is 256 rows of w where that still gives every SM a tile, else 128, and
 // where even those leave SMs idle a cluster shares each tile's K.
-Fp4Plan fp4_plan(int T, int N, int E, int num_kb, int num_sms) {
-  Fp4Plan p{2, 32, 1};
-  const int per = (T + E - 1) / E;
-  if (per > 96) {
-    p.bn = 192;
-    return p;
+static int max_clusters(int size) {
+  // per device and size, asked once: what a device can hold does not change
+  constexpr int kDevices = 64;
+  static std::atomic<int> known[kDevices][kMaxSplits + 1];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return 0;
+  const int have = known[dev][size].load(std::memory_order_relaxed);
+  if (have > 0) return have - 1;
+  using C = Cfg<true, false, 1, 32>;
+  auto* kernel = gemm_fp4_kernel<true, false, 1, 32, true>;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(size);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::kSmemBytes;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = size;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    n = 0;
   }
+  known[dev][size].store(n + 1, std::memory_order_relaxed);
+  return n;
+}
+
+Fp4Plan fp4_plan(int T, int N, int E, int num_kb, int num_sms) {
+  Fp4Plan p{32, 256, 1};
+  const int per = (T + E - 1) / E;
   if (per > 32) {
-    p.bn = 96;
+    p.tokens = per > 96 ? 192 : 96;
     return p;
   }
   const int experts = E < T ? E : T;
   if (static_cast<int64_t>(experts) * ((N + 255) / 256) >= num_sms) return p;
-  p.halves = 1;
+  p.cols = 128;
   const int tiles = experts * ((N + 127) / 128);
-  while (p.splits < kMaxSplits && tiles * p.splits * 2 <= num_sms && p.splits * 2 <= num_kb) p.splits *= 2;
+  // a cluster's CTAs sit in one GPC, whose SMs are no multiple of every size: a second round of
+  // clusters costs more than it brings (36 tiles, 4 CTAs each: 33 clusters fit, 14.7 us; 3 each XXX)
+  for (int s = kMaxSplits; s > 1; --s)
+    if (s <= num_kb && tiles <= max_clusters(s)) {
+      p.splits = s;
+      break;
+    }
   return p;
 }
 
-cudaError_t launch_gemm_fp4(int format, const CUtensorMap& tw, const CUtensorMap& tx, const Fp4GemmArgs& a,
+cudaError_t launch_gemm_fp4(int format, const CUtensorMap& tw, const CUtensorMap& tx, Fp4GemmArgs a, void* workspace,
                             const Fp4Plan& p, int num_sms, cudaStream_t s) {
   if (a.E > kMaxExperts) return cudaErrorInvalidValue;
+  a.ws_tiles = static_cast<uint8_t*>(workspace);
+  a.xs_tiles = a.ws_tiles + static_cast<int64_t>(a.num_kb) * a.E * a.m_tiles * tile_sf_bytes(format, p.cols);
   return format == kFp4Nv ? launch_fmt<true>(tw, tx, a, p, num_sms, s) : launch_fmt<false>(tw, tx, a, p, num_sms, s);
 }
 

@@ -356,6 +356,8 @@ struct Fp4GemmArgs {
   const uint8_t* ws;            // scales of w, rows ws_stride bytes apart
   int64_t xs_stride, ws_stride;
   int sf_cols;                  // scales per row: K / 32 or K / 16
+  uint8_t* xs_tiles;            // more than 32 tokens a tile: the scales by tiles, in the workspace
+  uint8_t* ws_tiles;
   const float* x_ts;            // tensor scale of x, or null
   const float* w_ts;            // tensor scale per expert, or null
   const int32_t* offsets;       // device [E + 1], or null (E = 1, all T rows)
@@ -369,13 +371,14 @@ struct Fp4GemmArgs {
   unsigned long long timeout_ns;
 };
 struct Fp4Plan {
-  int halves;                   // 128-row halves of w per tile
-  int bn;                       // token rows per tile
+  int tokens, cols;             // tile: rows of x, rows of w
   int splits;
 };
 Fp4Plan fp4_plan(int T, int N, int E, int num_kb, int num_sms);
-cudaError_t launch_gemm_fp4(int format, const CUtensorMap& tm_w, const CUtensorMap& tm_x, const Fp4GemmArgs& a,
-                            const Fp4Plan& p, int num_sms, cudaStream_t s);
+// Scratch that the plan needs (16-byte aligned), or 0.
+int64_t fp4_workspace(int format, int T, int N, int E, int num_kb, const Fp4Plan& p);
+cudaError_t launch_gemm_fp4(int format, const CUtensorMap& tm_w, const CUtensorMap& tm_x, Fp4GemmArgs a,
+                            void* workspace, const Fp4Plan& p, int num_sms, cudaStream_t s);
 
 // ---- self test
 cudaError_t launch_wait_timeout_probe(int* status, unsigned long long timeout_ns, cudaStream_t s);

@@ -51,6 +51,11 @@ moe_status check_route(const moe_route_config* c) {
 }
 
 bool fp4_format_ok(int32_t f) { return f == MOE_FP4_MX || f == MOE_FP4_NV; }
+bool product_shape_ok(int32_t T, int32_t N, int32_t K, int32_t E) {
+  return T >= 0 && N >= 1 && K >= 1 && E >= 1 && T <= 1 << 22 && N <= 1 << 18 && K <= 1 << 18 && E <= 512;
+}
+// Products whose tiles hold at most 32 tokens (fp4_plan): no workspace.
+bool few_rows(int32_t T, int32_t E) { return T <= 32ll * E; }
 
 }  // namespace
 
@@ -161,29 +166,44 @@ moe_status moe_fp4_pad_scales(const uint8_t* src, int64_t rows, int32_t cols, ui
   return launched(launch_pad_scales(src, rows, cols, dst, dst_stride, as_stream(stream)));
 }
 
+int64_t moe_fp4_workspace_bytes(int32_t format, int32_t T, int32_t N, int32_t K, int32_t E) {
+  if (!fp4_format_ok(format) || !product_shape_ok(T, N, K, E) || T == 0) return 0;
+  const int num_kb = (K + 255) / 256;
+  int dev = 0, sms = 0;
+  // without a device the shape alone decides, as on any
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    cudaGetLastError();
+  return fp4_workspace(format, T, N, E, num_kb, fp4_plan(T, N, E, num_kb, sms));
+}
+
 moe_status moe_fp4_matmul(const moe_fp4_product* p, moe_stream_t stream) {
   if (p == nullptr || !fp4_format_ok(p->format)) return MOE_ERR_INVALID_ARG;
   if (p->T < 0 || p->N < 1 || p->K < 1 || p->E < 1 || p->K % 32 != 0 || value_bytes(p->out_dtype) == 0)
     return MOE_ERR_INVALID_ARG;
   if (p->offsets == nullptr && p->E != 1) return MOE_ERR_INVALID_ARG;
   const int cols = p->K / (p->format == MOE_FP4_NV ? 16 : 32);
-  const int unit = p->format == MOE_FP4_NV ? 16 : 8;
-  if (p->x_scale_stride < cols || p->w_scale_stride < cols || p->x_scale_stride % unit != 0 ||
-      p->w_scale_stride % unit != 0)
-    return MOE_ERR_INVALID_ARG;
+  if (p->x_scale_stride < cols || p->w_scale_stride < cols) return MOE_ERR_INVALID_ARG;
   if (p->format == MOE_FP4_MX && (p->x_tensor_scale != nullptr || p->w_tensor_scale != nullptr))
     return MOE_ERR_INVALID_ARG;
-  if (p->T > 1 << 22 || p->N > 1 << 18 || p->K > 1 << 18 || p->E > 512) return MOE_ERR_UNSUPPORTED;
+  if (!product_shape_ok(p->T, p->N, p->K, p->E)) return MOE_ERR_UNSUPPORTED;
   if (p->T == 0) return MOE_OK;
   if (p->x == nullptr || p->x_scales == nullptr || p->w == nullptr || p->w_scales == nullptr || p->y == nullptr)
     return MOE_ERR_INVALID_ARG;
-  if (!aligned(p->x, 16) || !aligned(p->w, 16) || !aligned(p->x_scales, unit) || !aligned(p->w_scales, unit) ||
-      !aligned(p->y, value_bytes(p->out_dtype)) ||
+  if (!aligned(p->x, 16) || !aligned(p->w, 16) || !aligned(p->y, value_bytes(p->out_dtype)) ||
       !aligned(p->offsets, 4) || !aligned(p->x_tensor_scale, 4) || !aligned(p->w_tensor_scale, 4) ||
-      !aligned(p->status, 4))
+      !aligned(p->status, 4) || !aligned(p->workspace, 16))
     return MOE_ERR_INVALID_ARG;
+  if (few_rows(p->T, p->E)) {
+    const int unit = p->format == MOE_FP4_NV ? 16 : 8;
+    if (p->x_scale_stride % unit != 0 || p->w_scale_stride % unit != 0 || !aligned(p->x_scales, unit) ||
+        !aligned(p->w_scales, unit))
+      return MOE_ERR_INVALID_ARG;
+  } else if (p->workspace == nullptr) {
+    return MOE_ERR_INVALID_ARG;
+  }
   const moe_status st = on_device({p->x, p->x_scales, p->w, p->w_scales, p->y, p->offsets, p->x_tensor_scale,
-                                   p->w_tensor_scale, p->status});
+                                   p->w_tensor_scale, p->status, p->workspace});
   if (st != MOE_OK) return st;
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
@@ -207,13 +227,14 @@ moe_status moe_fp4_matmul(const moe_fp4_product* p, moe_stream_t stream) {
   a.status = p->status;
   a.timeout_ns = kWaitNs;
   const Fp4Plan plan = fp4_plan(p->T, p->N, p->E, a.num_kb, sms);
+  if (p->workspace_bytes < fp4_workspace(p->format, p->T, p->N, p->E, a.num_kb, plan)) return MOE_ERR_INVALID_ARG;
   a.splits = plan.splits;
-  a.m_tiles = (p->N + 128 * plan.halves - 1) / (128 * plan.halves);
+  a.m_tiles = (p->N + plan.cols - 1) / plan.cols;
   CUtensorMap tw, tx;
-  if (!encode_tmap_bytes(&tw, p->w, static_cast<uint64_t>(p->E) * p->N, p->K / 2, 128 * plan.halves) ||
+  if (!encode_tmap_bytes(&tw, p->w, static_cast<uint64_t>(p->E) * p->N, p->K / 2, plan.cols) ||
       !encode_tmap_bytes(&tx, p->x, p->T, p->K / 2, 32))
     return MOE_ERR_CUDA;
-  return launched(launch_gemm_fp4(p->format, tw, tx, a, plan, sms, as_stream(stream)));
+  return launched(launch_gemm_fp4(p->format, tw, tx, a, p->workspace, plan, sms, as_stream(stream)));
 }
 
 }  // extern "C"

@@ -178,7 +178,8 @@ def test_matmul_few_tokens(fmt, T, N, K):
 
 @pytest.mark.parametrize("fmt", FMT)
 @pytest.mark.parametrize("T,N,K", [(33, 256, 256), (64, 100, 320), (96, 1000, 1312), (97, 256, 512), (192, 512, 768),
-                                   (193, 300, 800), (500, 700, 2080), (1024, 2304, 512)])
+                                   (193, 300, 800), (500, 700, 2080), (1024, 2304, 512),
+                                   (515, 1001, 288), (777, 200, 96)])
 def test_matmul_many_tokens(fmt, T, N, K):
     _check_matmul(T, N, K, fmt)
 
@@ -186,7 +187,7 @@ def test_matmul_many_tokens(fmt, T, N, K):
 @pytest.mark.parametrize("fmt", FMT)
 @pytest.mark.parametrize("out", [torch.float32, torch.float16])
 def test_matmul_output_types(fmt, out):
-    for T in (7, 70, 210):
+    for T in (7, 70, 210, 530):
         _check_matmul(T, 333, 544, fmt, out)
 
 

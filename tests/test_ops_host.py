@@ -81,7 +81,7 @@ def test_fp4_refuses_bad_arguments(L):
 
 def _product(**kw):
     d = dict(format=0, T=4, N=64, K=64, E=1, out_dtype=0, x=FAKE, x_scales=FAKE, x_scale_stride=8, x_tensor_scale=None,
-             w=FAKE, w_scales=FAKE, w_scale_stride=8, w_tensor_scale=None, offsets=None, y=FAKE, status=None)
+             w=FAKE, w_scales=FAKE, w_scale_stride=8, w_tensor_scale=None, offsets=None, y=FAKE, workspace=None, workspace_bytes=0, status=None)
     d.update(kw)
     return moe._Fp4Product(*[d[n] for n, _ in moe._Fp4Product._fields_])
 
@@ -93,10 +93,14 @@ def _product(**kw):
     (dict(x_tensor_scale=FAKE), INV), (dict(w_tensor_scale=FAKE), INV), (dict(x=None), INV), (dict(w=FAKE + 8), INV),
     (dict(x=FAKE + 4), INV), (dict(y=FAKE + 1), INV), (dict(y=None), INV), (dict(w_scales=None), INV),
     (dict(offsets=FAKE + 2), INV), (dict(T=(1 << 22) + 1), UNS), (dict(E=513, offsets=FAKE), UNS),
-    (dict(N=(1 << 18) + 1), UNS), (dict(T=0, x=None, y=None), OK)])
+    (dict(N=(1 << 18) + 1), UNS), (dict(T=0, x=None, y=None), OK),
+    (dict(T=33), INV), (dict(T=33, workspace=FAKE + 8), INV)])
 def test_fp4_matmul_refuses_bad_arguments(L, kw, want):
     assert L.moe_fp4_matmul(_product(**kw), None) == want
     assert L.moe_fp4_matmul(None, None) == INV
+    w = L.moe_fp4_workspace_bytes
+    assert w(0, 32, 64, 64, 1) == 0 and w(1, 33, 64, 64, 1) > 0 and w(0, 64, 64, 64, 2) == 0 and w(2, 99, 64, 64, 1) == 0
+    assert w(0, -1, 64, 64, 1) == 0 and w(0, 99, 0, 64, 1) == 0 and w(0, 99, 64, 64, 513) == 0
 
 
 def test_bindings_refuse_bad_tensors(L):
