@@ -343,25 +343,22 @@ __device__ __forceinline__ void store_pairs(const Fp4GemmArgs& a, int row0, int 
       out[static_cast<int64_t>(j) * a.N + n] = static_cast<uint16_t>(p[j / 2] >> (16 * (j & 1)));
 }
 
-// 16 accumulator columns (tokens) c0 .. c0 + 15 of row m of the tile, scaled and stored.
-__device__ __forceinline__ void store_16(const Fp4GemmArgs& a, const Tile& tl, int m, int c0, int lane, bool vec,
-                                         float alpha, const uint32_t (&r)[16]) {
-  if (a.out_dtype == kValFp32) {
-    float* p = static_cast<float*>(a.out) + static_cast<int64_t>(tl.row0 + c0) * a.N + tl.col0 + m;
-    if (m < tl.cols) {
+// 16 accumulator columns (tokens) scaled and rounded to 16 bits, as pairs.
+__device__ __forceinline__ void pack_16(bool bf, float alpha, const uint32_t (&r)[16], uint32_t (&v)[8]) {
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        if (c0 + j < tl.rows) *p = alpha * __uint_as_float(r[j]);
-        p += a.N;
-      }
-    }
-    return;
+  for (int j = 0; j < 8; ++j)
+    v[j] = pack_pair(bf, alpha * __uint_as_float(r[2 * j]), alpha * __uint_as_float(r[2 * j + 1]));
+}
+// The same in 32 bits, stored: tokens c0 .. c0 + 15 of row m of the tile.
+__device__ __forceinline__ void store_f32(const Fp4GemmArgs& a, const Tile& tl, int m, int c0, float alpha,
+                                          const uint32_t (&r)[16]) {
+  if (m >= tl.cols) return;
+  float* p = static_cast<float*>(a.out) + static_cast<int64_t>(tl.row0 + c0) * a.N + tl.col0 + m;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    if (c0 + j < tl.rows) *p = alpha * __uint_as_float(r[j]);
+    p += a.N;
   }
-  const bool bf = a.out_dtype == kValBf16;
-  uint32_t v[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = pack_pair(bf, alpha * __uint_as_float(r[2 * j]), alpha * __uint_as_float(r[2 * j + 1]));
-  store_pairs(a, tl.row0, c0, tl.rows, tl.col0 + m, lane, vec, v);
 }
 
 template <bool kNv, bool kPre, int kHalves, int kBN, bool kSplit>
@@ -726,19 +723,51 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float alpha = args.w_ts ? xts * __ldg(args.w_ts + tl.g) : xts;
         const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * C::kAccCols;
         const int mine = q * 32 + lane;  // this lane's row of the tile's first half
+        if (args.out_dtype == kValFp32) {
 #pragma unroll 1
-        for (int c0 = cfirst; c0 < tl.rows; c0 += 16 * C::kEpiGroups) {
+          for (int c0 = cfirst; c0 < tl.rows; c0 += 16 * C::kEpiGroups) {
 #pragma unroll 1
-          for (int h = 0; h < kHalves; ++h) {
-            uint32_t r[16];
-            tmem_ld16(tb + h * kBN + c0, r);
-            tmem_ld_wait();
-            store_16(args, tl, mine + h * 128, c0, lane, vec_out, alpha, r);
+            for (int h = 0; h < kHalves; ++h) {
+              uint32_t r[16];
+              tmem_ld16(tb + h * kBN + c0, r);
+              tmem_ld_wait();
+              store_f32(args, tl, mine + h * 128, c0, alpha, r);
+            }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&tempty[acc]);
+        } else {
+          // 16-bit results fit in registers as pairs: take the whole tile out of TMEM, give it back to
+          // the MMAs, and store while the next tile's run
+          constexpr int kChunks = (kBN / 16 + C::kEpiGroups - 1) / C::kEpiGroups;
+          const bool bf = args.out_dtype == kValBf16;
+          uint32_t hold[kChunks][kHalves][8];
+#pragma unroll
+          for (int i = 0; i < kChunks; ++i) {
+            const int c0 = cfirst + i * 16 * C::kEpiGroups;
+            if (c0 < tl.rows) {
+              uint32_t r[kHalves][16];
+#pragma unroll
+              for (int h = 0; h < kHalves; ++h) tmem_ld16(tb + h * kBN + c0, r[h]);
+              tmem_ld_wait();
+#pragma unroll
+              for (int h = 0; h < kHalves; ++h) pack_16(bf, alpha, r[h], hold[i][h]);
+            }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&tempty[acc]);
+#pragma unroll
+          for (int i = 0; i < kChunks; ++i) {
+            const int c0 = cfirst + i * 16 * C::kEpiGroups;
+            if (c0 < tl.rows) {
+#pragma unroll
+              for (int h = 0; h < kHalves; ++h)
+                store_pairs(args, tl.row0, c0, tl.rows, tl.col0 + mine + h * 128, lane, vec_out, hold[i][h]);
+            }
           }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&tempty[acc]);
       }
       if (++acc == C::kAccs) {
         acc = 0;
@@ -780,7 +809,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float alpha = args.w_ts ? xts * __ldg(args.w_ts + tl.g) : xts;
       const int m = q * 32 + lane;
       const bool vec_out = args.N % 4 == 0 && (reinterpret_cast<uintptr_t>(args.out) & 7) == 0;
-      store_16(args, tl, m, cfirst, lane, vec_out, alpha, r);
+      if (args.out_dtype == kValFp32) {
+        store_f32(args, tl, m, cfirst, alpha, r);
+      } else {
+        uint32_t v[8];
+        pack_16(args.out_dtype == kValBf16, alpha, r, v);
+        store_pairs(args, tl.row0, cfirst, tl.rows, tl.col0 + m, lane, vec_out, v);
+      }
     }
   }
   tc_fence_before();
