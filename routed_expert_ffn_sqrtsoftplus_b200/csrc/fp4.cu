@@ -8,9 +8,9 @@
 //   Elements are the nearest E2M1, ties to the even code, at most 6 in magnitude. A block that
 //   holds NaN or infinity gets the scale format's NaN, so that it reads back as NaN.
 //
-// Every decision is the exact one: MXFP4 divides by a power of two; for NVFP4 a quotient that
-// comes near a border of the grid is decided by the sign of |x| - border * d in one fused
-// multiply-add, which rounds to zero only what is zero.
+// Every decision is the exact one: MXFP4 divides by a power of two; for NVFP4 a block with a
+// quotient near a border of the grid is decided by the signs of |x| - border * d in one fused
+// multiply-add each, which rounds to zero only what is zero.
 //
 // Bound by HBM: 2 (or 4) bytes in and 0.5 + 1/16 (or 1/32) out per value. A thread takes 16
 // consecutive values (an NVFP4 block, or half an MXFP4 block whose other half is the
@@ -27,10 +27,26 @@ namespace {
 
 constexpr int kRun = 16;  // values per thread
 
-template <typename T>
-__device__ __forceinline__ void load16(const T* p, bool vec, float (&v)[kRun]);
-template <>
-__device__ __forceinline__ void load16<float>(const float* p, bool vec, float (&v)[kRun]) {
+// n / d for n < 2^31 by a multiplication (the row of a run; a division costs as much as a value's
+// whole conversion).
+struct FastDiv {
+  uint32_t mul, shift, d;
+};
+FastDiv fast_div(uint32_t d) {
+  FastDiv f{0, 0, d};
+  while ((uint64_t(1) << f.shift) < d) ++f.shift;
+  f.mul = static_cast<uint32_t>(((uint64_t(1) << 32) * ((uint64_t(1) << f.shift) - d)) / d + 1);
+  return f;
+}
+__device__ __forceinline__ uint32_t divide(uint32_t n, const FastDiv& f) { return (__umulhi(n, f.mul) + n) >> f.shift; }
+
+__device__ __forceinline__ float value_f32(float v) { return v; }
+__device__ __forceinline__ float value_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float value_f32(__half v) { return __half2float(v); }
+
+// 16 consecutive values and the largest magnitude among them; not finite: false. Magnitudes are
+// compared as integers, in which infinity and NaN come last, two 16-bit values at a time.
+__device__ __forceinline__ bool load16(const float* p, bool vec, float (&v)[kRun], float& amax) {
   if (vec) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -44,37 +60,57 @@ __device__ __forceinline__ void load16<float>(const float* p, bool vec, float (&
 #pragma unroll
     for (int i = 0; i < kRun; ++i) v[i] = __ldg(p + i);
   }
+  uint32_t m = 0u;
+#pragma unroll
+  for (int i = 0; i < kRun; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+  amax = __uint_as_float(m);
+  return m < 0x7F800000u;
 }
-template <typename T, typename T2>
-__device__ __forceinline__ void load16_half(const T* p, bool vec, float (&v)[kRun], float2 (*to2)(T2),
-                                            float (*to1)(T)) {
+template <typename T>
+__device__ __forceinline__ bool load16_half(const T* p, bool vec, uint32_t (&w)[8], uint32_t infinity, uint32_t& m) {
   if (vec) {
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
       const uint4 u = __ldg(reinterpret_cast<const uint4*>(p) + q);
-      const T2* h = reinterpret_cast<const T2*>(&u);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 f = to2(h[i]);
-        v[8 * q + 2 * i] = f.x;
-        v[8 * q + 2 * i + 1] = f.y;
-      }
+      w[4 * q] = u.x;
+      w[4 * q + 1] = u.y;
+      w[4 * q + 2] = u.z;
+      w[4 * q + 3] = u.w;
     }
   } else {
+    const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
 #pragma unroll
-    for (int i = 0; i < kRun; ++i) v[i] = to1(p[i]);
+    for (int i = 0; i < 8; ++i)
+      w[i] = static_cast<uint32_t>(__ldg(h + 2 * i)) | static_cast<uint32_t>(__ldg(h + 2 * i + 1)) << 16;
   }
+  uint32_t mm = 0u;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) mm = __vmaxu2(mm, w[i] & 0x7FFF7FFFu);
+  m = max(mm & 0xFFFFu, mm >> 16);
+  return m < infinity;
 }
-template <>
-__device__ __forceinline__ void load16<__nv_bfloat16>(const __nv_bfloat16* p, bool vec, float (&v)[kRun]) {
-  load16_half<__nv_bfloat16, __nv_bfloat162>(
-      p, vec, v, [](__nv_bfloat162 h) { return __bfloat1622float2(h); },
-      [](__nv_bfloat16 h) { return __bfloat162float(h); });
+__device__ __forceinline__ bool load16(const __nv_bfloat16* p, bool vec, float (&v)[kRun], float& amax) {
+  uint32_t w[8], m;
+  const bool finite = load16_half(p, vec, w, 0x7F80u, m);
+  amax = __uint_as_float(m << 16);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+  return finite;
 }
-template <>
-__device__ __forceinline__ void load16<__half>(const __half* p, bool vec, float (&v)[kRun]) {
-  load16_half<__half, __half2>(
-      p, vec, v, [](__half2 h) { return __half22float2(h); }, [](__half h) { return __half2float(h); });
+__device__ __forceinline__ bool load16(const __half* p, bool vec, float (&v)[kRun], float& amax) {
+  uint32_t w[8], m;
+  const bool finite = load16_half(p, vec, w, 0x7C00u, m);
+  amax = __half2float(__ushort_as_half(static_cast<unsigned short>(m)));
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+    v[2 * i] = f.x;
+    v[2 * i + 1] = f.y;
+  }
+  return finite;
 }
 
 // E4M3 value of a non-negative code (0 .. 126).
@@ -86,177 +122,188 @@ __device__ __forceinline__ float e4m3_value(int code) {
 
 // The E4M3 code nearest to amax / (6 ts), ties to even, at most 126 (448).
 __device__ __forceinline__ int e4m3_scale(float amax, float ts) {
-  int c = static_cast<int>(__nv_cvt_float_to_fp8(__fdiv_rn(amax, 6.0f * ts), __NV_SATFINITE, __NV_E4M3)) & 0x7F;
-  // the quotient was rounded: look at the borders on both sides, 6 * midpoint * ts, whose first
-  // product is exact in 32 bits
+  const float q = amax * __frcp_rn(6.0f * ts);  // off by a few units of 2^-24: the code is right, or a neighbour
+  int c = static_cast<int>(__nv_cvt_float_to_fp8(q, __NV_SATFINITE, __NV_E4M3)) & 0x7F;
+  c = min(c, 126);
+  // the borders on both sides, 6 * midpoint * ts: the first product is exact in 32 bits, and the fused
+  // multiply-add keeps the difference's sign
+  const float v = e4m3_value(c);
   if (c < 126) {
-    const float mid = 0.5f * (e4m3_value(c) + e4m3_value(c + 1));
-    const float s = fmaf(-6.0f * mid, ts, amax);
+    const float s = fmaf(-3.0f * (v + e4m3_value(c + 1)), ts, amax);
     if (s > 0.f || (s == 0.f && (c & 1))) return c + 1;
   }
   if (c > 0) {
-    const float mid = 0.5f * (e4m3_value(c) + e4m3_value(c - 1));
-    const float s = fmaf(-6.0f * mid, ts, amax);
+    const float s = fmaf(-3.0f * (v + e4m3_value(c - 1)), ts, amax);
     if (s < 0.f || (s == 0.f && (c & 1))) return c - 1;
   }
   return c;
 }
 
-// E2M1 magnitude code of a against the element unit d, decided exactly.
-__device__ __forceinline__ uint32_t e2m1_exact(float a, float d) {
-  return (fmaf(-0.25f, d, a) > 0.f) + (fmaf(-0.75f, d, a) >= 0.f) + (fmaf(-1.25f, d, a) > 0.f) +
-         (fmaf(-1.75f, d, a) >= 0.f) + (fmaf(-2.5f, d, a) > 0.f) + (fmaf(-3.5f, d, a) >= 0.f) +
-         (fmaf(-5.0f, d, a) > 0.f);
+// Eight scaled values to a word of E2M1 codes, the first in the lowest nibble: nearest, ties to even, at most 6.
+__device__ __forceinline__ uint32_t to_e2m1x8(const float* v, float scale) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}\n"
+      : "=r"(r)
+      : "f"(v[0] * scale), "f"(v[1] * scale), "f"(v[2] * scale), "f"(v[3] * scale), "f"(v[4] * scale),
+        "f"(v[5] * scale), "f"(v[6] * scale), "f"(v[7] * scale));
+  return r;
 }
 
-// Whether q, rounded from an exact quotient, may sit on the other side of a border of the E2M1
-// grid: every border has at most three significant bits, so the low 21 bits of its float are 0.
-// (A quotient of 0 comes from a value of 0, or from one far below the first border.)
-__device__ __forceinline__ bool near_border(float q) {
-  return ((__float_as_uint(q) + 2u) & 0x1FFFFFu) <= 4u && q != 0.f;
+// Decides the codes in which `lo` and `hi`, neighbours on the grid, differ: value j against the border
+// between them, border * d, by the sign of one fused multiply-add. The few values are read again (an
+// index into registers would put them all into local memory).
+template <typename T>
+__device__ __forceinline__ uint32_t settle(uint32_t lo, uint32_t hi, const T* p, float d) {
+  for (uint32_t diff = lo ^ hi; diff != 0u;) {
+    const int at = (__ffs(static_cast<int>(diff)) - 1) & ~3;
+    const uint32_t c = (lo >> at) & 7u;
+    // (grid[c] + grid[c + 1]) / 2: 1/4 + c/2 up to 7/4, then 5/2, 7/2, 5
+    const float border = c < 4u ? 0.25f + 0.5f * static_cast<float>(c) : c < 6u ? static_cast<float>(c) - 1.5f : 5.0f;
+    const float s = fmaf(-border, d, fabsf(value_f32(p[at / 4])));
+    if (s > 0.f || (s == 0.f && (c & 1u))) lo += 1u << at;
+    diff &= ~(0xFu << at);
+  }
+  return lo;
 }
 
 template <typename T, bool kNv>
 __global__ void __launch_bounds__(256)
-    quantize_fp4_kernel(const T* __restrict__ src, int64_t runs, int runs_per_row, int64_t row_stride, int vec,
+    quantize_fp4_kernel(const T* __restrict__ src, uint32_t runs, FastDiv per_row, int64_t row_stride, int vec,
                         const float* __restrict__ tensor_scale, uint2* __restrict__ codes,
                         uint8_t* __restrict__ scales, int64_t scale_stride) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-  // cols % 32 == 0: an even number of runs, so a lane and its neighbour are in range together
+  const uint32_t i = blockIdx.x * 256u + threadIdx.x;
+  // cols % 32 == 0: an even number of runs, so that a lane and its neighbour are in range together
   if (i >= runs) return;
-  const int64_t row = i / runs_per_row;
-  const int run = static_cast<int>(i - row * runs_per_row);
-  float v[kRun];
-  load16<T>(src + row * row_stride + static_cast<int64_t>(run) * kRun, vec != 0, v);
-  float amax = 0.f;
-  bool finite = true;
-#pragma unroll
-  for (int j = 0; j < kRun; ++j) {
-    const float a = fabsf(v[j]);
-    finite = finite && a < INFINITY;
-    amax = fmaxf(amax, a);
-  }
+  const uint32_t row = divide(i, per_row);
+  const uint32_t run = i - row * per_row.d;
+  float v[kRun], amax;
+  bool finite = load16(src + row * row_stride + run * kRun, vec != 0, v, amax);
   uint32_t w[2] = {0u, 0u};
   if constexpr (!kNv) {
     const unsigned pair = 3u << ((threadIdx.x & 31) & ~1);
-    amax = fmaxf(amax, __shfl_xor_sync(pair, amax, 1));
-    finite = __shfl_xor_sync(pair, finite ? 1 : 0, 1) != 0 && finite;
+    // a block that is not finite is one as a whole: the larger magnitude, compared as an integer
+    const uint32_t m = max(__float_as_uint(amax), __shfl_xor_sync(pair, __float_as_uint(amax), 1));
+    finite = m < 0x7F800000u;
     int code;
     float inv;
-    mx_scale(amax, 2, code, inv);
+    mx_scale(__uint_as_float(m), 2, code, inv);
+    // a power of two: the products are exact, and the conversion rounds them as the format asks
+    w[0] = to_e2m1x8(v, inv);
+    w[1] = to_e2m1x8(v + 8, inv);
     if (!finite) {
       code = 0xFF;
-      inv = 0.f;
-    }
-    // a power of two: the products are exact, and the conversion rounds them as the format asks
-#pragma unroll
-    for (int j = 0; j < kRun / 2; ++j) {
-      const float2 f = finite ? make_float2(v[2 * j] * inv, v[2 * j + 1] * inv) : make_float2(0.f, 0.f);
-      w[j / 4] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp4x2(f, __NV_E2M1, cudaRoundNearest)) << (8 * (j % 4));
+      w[0] = w[1] = 0u;
     }
     if ((run & 1) == 0) scales[row * scale_stride + run / 2] = static_cast<uint8_t>(code);
   } else {
     const float ts = tensor_scale ? __ldg(tensor_scale) : 1.0f;
     const int code = finite ? e4m3_scale(amax, ts) : 0x7F;
     const float d = finite ? e4m3_value(code) * ts : 0.f;
-    if (d > 0.f) {
-      const float inv = __fdiv_rn(1.0f, d);
-      bool near = false;
-#pragma unroll
-      for (int j = 0; j < kRun / 2; ++j) {
-        const float2 f = make_float2(v[2 * j] * inv, v[2 * j + 1] * inv);
-        near = near || near_border(f.x) || near_border(f.y);
-        w[j / 4] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp4x2(f, __NV_E2M1, cudaRoundNearest)) << (8 * (j % 4));
-      }
-      // a unit that is a power of two leaves the quotients exact
-      if (near && (__float_as_uint(d) & 0x7FFFFFu) != 0u) {
-        w[0] = w[1] = 0u;
-#pragma unroll
-        for (int j = 0; j < kRun; ++j)
-          w[j / 8] |= (e2m1_exact(fabsf(v[j]), d) | (signbit(v[j]) ? 8u : 0u)) << (4 * (j % 8));
-      }
+    const uint32_t db = __float_as_uint(d);
+    if (db >= 0x00800000u && db < 0x7F800000u) {  // a unit below the normal range counts as 0
+      // Quotients by two reciprocals, one a little low, one a little high: where both give the same
+      // codes, so does the exact quotient. (A unit that is a power of two divides exactly.)
+      const bool pow2 = (db & 0x7FFFFFu) == 0u && db >= 0x01000000u && db <= 0x7E000000u;
+      const float inv = pow2 ? __uint_as_float(0x7F000000u - db) : __fdividef(1.0f, d);
+      const float lo = pow2 ? inv : inv * (1.0f - 0x1p-20f), hi = pow2 ? inv : inv * (1.0f + 0x1p-20f);
+      w[0] = to_e2m1x8(v, lo);
+      w[1] = to_e2m1x8(v + 8, lo);
+      const uint32_t u0 = to_e2m1x8(v, hi), u1 = to_e2m1x8(v + 8, hi);
+      // Real tensors do come near borders: a tensor scale taken from a 16-bit maximum puts many blocks'
+      // units at simple fractions of their values (1.5 % of the runs of normally distributed rows).
+      const T* p = src + row * row_stride + run * kRun;
+      w[0] = settle(w[0], u0, p, d);
+      w[1] = settle(w[1], u1, p + 8, d);
     }
     scales[row * scale_stride + run] = static_cast<uint8_t>(code);
   }
   codes[i] = make_uint2(w[0], w[1]);
 }
 
-template <typename T>
-__device__ __forceinline__ void store16(T* p, const float (&v)[kRun], bool vec);
-template <>
-__device__ __forceinline__ void store16<float>(float* p, const float (&v)[kRun], bool vec) {
+// Eight consecutive values.
+__device__ __forceinline__ void store8(float* p, const float (&v)[8], bool vec) {
   if (vec) {
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      reinterpret_cast<float4*>(p)[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+    reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
   } else {
 #pragma unroll
-    for (int i = 0; i < kRun; ++i) p[i] = v[i];
+    for (int i = 0; i < 8; ++i) p[i] = v[i];
   }
 }
-template <>
-__device__ __forceinline__ void store16<__nv_bfloat16>(__nv_bfloat16* p, const float (&v)[kRun], bool vec) {
-  __nv_bfloat162 h[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) h[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+template <typename T2, typename T>
+__device__ __forceinline__ void store8_half(T* p, const T2 (&h)[4], bool vec) {
   if (vec) {
-    reinterpret_cast<uint4*>(p)[0] = *reinterpret_cast<uint4*>(h);
-    reinterpret_cast<uint4*>(p)[1] = *reinterpret_cast<uint4*>(h + 4);
+    *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(h);
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 4; ++i) {
       p[2 * i] = h[i].x;
       p[2 * i + 1] = h[i].y;
     }
   }
 }
-template <>
-__device__ __forceinline__ void store16<__half>(__half* p, const float (&v)[kRun], bool vec) {
-  __half2 h[8];
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8], bool vec) {
+  __align__(16) __nv_bfloat162 h[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) h[i] = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
-  if (vec) {
-    reinterpret_cast<uint4*>(p)[0] = *reinterpret_cast<uint4*>(h);
-    reinterpret_cast<uint4*>(p)[1] = *reinterpret_cast<uint4*>(h + 4);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      p[2 * i] = h[i].x;
-      p[2 * i + 1] = h[i].y;
-    }
-  }
+  for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+  store8_half(p, h, vec);
 }
+__device__ __forceinline__ void store8(__half* p, const float (&v)[8], bool vec) {
+  __align__(16) __half2 h[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) h[i] = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+  store8_half(p, h, vec);
+}
+
+// A thread takes eight values, so that a warp's 16-byte stores adjoin, and kSteps such pieces a
+// block's width apart, loaded together.
+constexpr int kSteps = 4;
 
 template <typename T, bool kNv>
 __global__ void __launch_bounds__(256)
-    dequantize_fp4_kernel(const uint2* __restrict__ codes, const uint8_t* __restrict__ scales, int64_t runs,
-                          int runs_per_row, int64_t scale_stride, const float* __restrict__ tensor_scale, int vec,
+    dequantize_fp4_kernel(const uint32_t* __restrict__ codes, const uint8_t* __restrict__ scales, uint32_t pieces,
+                          FastDiv per_row, int64_t scale_stride, const float* __restrict__ tensor_scale, int vec,
                           T* __restrict__ dst) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-  if (i >= runs) return;
-  const int64_t row = i / runs_per_row;
-  const int run = static_cast<int>(i - row * runs_per_row);
-  const uint2 c = __ldg(codes + i);
-  const uint32_t s = __ldg(scales + row * scale_stride + (kNv ? run : run / 2));
-  float d;
-  if constexpr (kNv) {
-    // the sign bit of a scale is not used by the format
-    d = (s & 0x7Fu) == 0x7Fu ? __int_as_float(0x7fc00000) : e4m3_value(static_cast<int>(s & 0x7Fu));
-    if (tensor_scale) d *= __ldg(tensor_scale);
-  } else {
-    d = s == 0xFFu ? __int_as_float(0x7fc00000) : __uint_as_float(s == 0u ? 1u << 22 : s << 23);
-  }
-  float v[kRun];
+  constexpr uint32_t kPerScale = kNv ? 2 : 4;  // pieces of a block
+  const uint32_t first = blockIdx.x * (256u * kSteps) + threadIdx.x;
+  uint32_t c[kSteps], sc[kSteps];
 #pragma unroll
-  for (int j = 0; j < kRun / 2; ++j) {
-    const uint32_t w = j < 4 ? c.x : c.y;
-    const __half2_raw h =
-        __nv_cvt_fp4x2_to_halfraw2(static_cast<__nv_fp4x2_storage_t>((w >> (8 * (j % 4))) & 0xFFu), __NV_E2M1);
-    const float2 f = __half22float2(__half2(h));
-    v[2 * j] = f.x * d;
-    v[2 * j + 1] = f.y * d;
+  for (int u = 0; u < kSteps; ++u) {
+    const uint32_t i = first + 256u * u;
+    c[u] = sc[u] = 0u;
+    if (i < pieces) {
+      c[u] = __ldg(codes + i);
+      const uint32_t row = divide(i, per_row);
+      sc[u] = __ldg(scales + row * scale_stride + (i - row * per_row.d) / kPerScale);
+    }
   }
-  store16<T>(dst + i * kRun, v, vec != 0);
+  const float ts = kNv && tensor_scale ? __ldg(tensor_scale) : 1.0f;
+#pragma unroll
+  for (int u = 0; u < kSteps; ++u) {
+    const uint32_t i = first + 256u * u;
+    if (i >= pieces) break;
+    const uint32_t s = sc[u];
+    float d;
+    if constexpr (kNv) {
+      // the sign bit of a scale is not used by the format
+      d = (s & 0x7Fu) == 0x7Fu ? __int_as_float(0x7fc00000) : e4m3_value(static_cast<int>(s & 0x7Fu)) * ts;
+    } else {
+      d = s == 0xFFu ? __int_as_float(0x7fc00000) : __uint_as_float(s == 0u ? 1u << 22 : s << 23);
+    }
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const __half2_raw h =
+          __nv_cvt_fp4x2_to_halfraw2(static_cast<__nv_fp4x2_storage_t>((c[u] >> (8 * j)) & 0xFFu), __NV_E2M1);
+      const float2 f = __half22float2(__half2(h));
+      v[2 * j] = f.x * d;
+      v[2 * j + 1] = f.y * d;
+    }
+    store8(dst + static_cast<int64_t>(i) * 8, v, vec != 0);
+  }
 }
 
 // Scale rows into rows of another stride, 4 bytes of the destination per thread.
@@ -278,11 +325,10 @@ __global__ void __launch_bounds__(256)
 template <typename T, bool kNv>
 cudaError_t quantize_t(const void* src, int64_t rows, int cols, int64_t row_stride, const float* ts, uint8_t* codes,
                        uint8_t* scales, int64_t scale_stride, cudaStream_t s) {
-  const int rpr = cols / kRun;
-  const int64_t runs = rows * rpr;
+  const uint32_t rpr = cols / kRun, runs = static_cast<uint32_t>(rows * rpr);
   const bool vec = reinterpret_cast<uintptr_t>(src) % 16 == 0 && (row_stride * sizeof(T)) % 16 == 0;
-  quantize_fp4_kernel<T, kNv><<<static_cast<unsigned>((runs + 255) / 256), 256, 0, s>>>(
-      static_cast<const T*>(src), runs, rpr, row_stride, vec ? 1 : 0, ts, reinterpret_cast<uint2*>(codes), scales,
+  quantize_fp4_kernel<T, kNv><<<(runs + 255) / 256, 256, 0, s>>>(
+      static_cast<const T*>(src), runs, fast_div(rpr), row_stride, vec ? 1 : 0, ts, reinterpret_cast<uint2*>(codes), scales,
       scale_stride);
   return cudaGetLastError();
 }
@@ -290,11 +336,11 @@ cudaError_t quantize_t(const void* src, int64_t rows, int cols, int64_t row_stri
 template <typename T, bool kNv>
 cudaError_t dequantize_t(const uint8_t* codes, const uint8_t* scales, int64_t rows, int cols, int64_t scale_stride,
                          const float* ts, void* dst, cudaStream_t s) {
-  const int rpr = cols / kRun;
-  const int64_t runs = rows * rpr;
+  const uint32_t ppr = cols / 8, pieces = static_cast<uint32_t>(rows * ppr);
   const bool vec = reinterpret_cast<uintptr_t>(dst) % 16 == 0;
-  dequantize_fp4_kernel<T, kNv><<<static_cast<unsigned>((runs + 255) / 256), 256, 0, s>>>(
-      reinterpret_cast<const uint2*>(codes), scales, runs, rpr, scale_stride, ts, vec ? 1 : 0, static_cast<T*>(dst));
+  dequantize_fp4_kernel<T, kNv><<<(pieces + 256 * kSteps - 1) / (256 * kSteps), 256, 0, s>>>(
+      reinterpret_cast<const uint32_t*>(codes), scales, pieces, fast_div(ppr), scale_stride, ts, vec ? 1 : 0,
+      static_cast<T*>(dst));
   return cudaGetLastError();
 }
 

@@ -128,7 +128,7 @@ moe_status moe_quantize_fp4(int32_t format, const void* src, int32_t dtype, int6
     return MOE_ERR_INVALID_ARG;
   if (scale_stride < cols / (format == MOE_FP4_NV ? 16 : 32)) return MOE_ERR_INVALID_ARG;
   if (format == MOE_FP4_MX && tensor_scale != nullptr) return MOE_ERR_INVALID_ARG;
-  if (rows > (int64_t(1) << 38) / cols) return MOE_ERR_UNSUPPORTED;
+  if (rows > (int64_t(1) << 33) / cols) return MOE_ERR_UNSUPPORTED;
   if (rows == 0) return MOE_OK;
   if (src == nullptr || codes == nullptr || scales == nullptr) return MOE_ERR_INVALID_ARG;
   if (!aligned(src, vb) || !aligned(codes, 16) || !aligned(tensor_scale, 4)) return MOE_ERR_INVALID_ARG;
@@ -145,7 +145,7 @@ moe_status moe_dequantize_fp4(int32_t format, const uint8_t* codes, const uint8_
   if (!fp4_format_ok(format) || vb == 0 || rows < 0 || cols <= 0 || cols % 32 != 0) return MOE_ERR_INVALID_ARG;
   if (scale_stride < cols / (format == MOE_FP4_NV ? 16 : 32)) return MOE_ERR_INVALID_ARG;
   if (format == MOE_FP4_MX && tensor_scale != nullptr) return MOE_ERR_INVALID_ARG;
-  if (rows > (int64_t(1) << 38) / cols) return MOE_ERR_UNSUPPORTED;
+  if (rows > (int64_t(1) << 33) / cols) return MOE_ERR_UNSUPPORTED;
   if (rows == 0) return MOE_OK;
   if (codes == nullptr || scales == nullptr || dst == nullptr) return MOE_ERR_INVALID_ARG;
   if (!aligned(codes, 16) || !aligned(dst, vb) || !aligned(tensor_scale, 4)) return MOE_ERR_INVALID_ARG;
