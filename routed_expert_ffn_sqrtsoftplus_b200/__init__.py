@@ -281,11 +281,11 @@ def route(logits: torch.Tensor, top_k: int, *, score: str = "softmax", bias: Opt
         _need(bias, "bias", torch.float32, (E,))
     cfg = _route_config(E, top_k, n_groups, topk_groups, score, group_score, renormalize, route_scale)
     if topk_idx is None:
-        topk_idx = torch.empty((T, top_k), dtype=torch.int32, device=logits.device)
+        topk_idx = logits.new_empty((T, top_k), dtype=torch.int32)
     else:
         _need(topk_idx, "topk_idx", torch.int32, (T, top_k))
     if topk_w is None:
-        topk_w = torch.empty((T, top_k), dtype=torch.float32, device=logits.device)
+        topk_w = logits.new_empty((T, top_k), dtype=torch.float32)
     else:
         _need(topk_w, "topk_w", torch.float32, (T, top_k))
     _same_device(logits, bias=bias, topk_idx=topk_idx, topk_w=topk_w)
@@ -308,7 +308,7 @@ def route_backward(grad_w: torch.Tensor, logits: torch.Tensor, topk_idx: torch.T
     _need(grad_w, "grad_w", torch.float32, (T, k))
     cfg = _route_config(E, k, 1, 1, score, "max", renormalize, route_scale)
     if out is None:
-        out = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
+        out = logits.new_empty((T, E))
     else:
         _need(out, "out", logits.dtype, (T, E))
     _same_device(logits, grad_w=grad_w, topk_idx=topk_idx, out=out)
@@ -350,8 +350,8 @@ def quantize_fp4(x: torch.Tensor, fmt: str, tensor_scale: Optional[torch.Tensor]
     ts = _tensor_scale(tensor_scale, "tensor_scale", fmt, 1)
     _same_device(x, tensor_scale=tensor_scale)
     sc = K // FP4_BLOCK[fmt]
-    codes = torch.empty((rows, K // 2), dtype=torch.uint8, device=x.device)
-    scales = torch.empty((rows, sc), dtype=torch.uint8, device=x.device)
+    codes = x.new_empty((rows, K // 2), dtype=torch.uint8)
+    scales = x.new_empty((rows, sc), dtype=torch.uint8)
     _check(lib().moe_quantize_fp4(f, x.data_ptr(), code, rows, K, rs, ts, codes.data_ptr(), scales.data_ptr(), sc,
                                   _current(x)), "moe_quantize_fp4")
     return codes, scales
@@ -375,7 +375,7 @@ def dequantize_fp4(codes: torch.Tensor, scales: torch.Tensor, fmt: str, tensor_s
     _need(scales, "scales", torch.uint8, (rows, K // FP4_BLOCK[fmt]))
     ts = _tensor_scale(tensor_scale, "tensor_scale", fmt, 1)
     _same_device(codes, scales=scales, tensor_scale=tensor_scale)
-    out = torch.empty((rows, K), dtype=dtype, device=codes.device)
+    out = codes.new_empty((rows, K), dtype=dtype)
     _check(lib().moe_dequantize_fp4(f, codes.data_ptr(), scales.data_ptr(), rows, K, scales.shape[1], ts,
                                     out.data_ptr(), _VALUE_DTYPES[dtype], _current(codes)), "moe_dequantize_fp4")
     return out
@@ -396,7 +396,7 @@ def _fp4_weights(w, w_scales, fmt, K, offsets):
 
 def _fp4_out(x, T, N, out, out_dtype):
     if out is None:
-        return torch.empty((T, N), dtype=out_dtype, device=x.device)
+        return x.new_empty((T, N), dtype=out_dtype)
     if out.dtype not in _VALUE_DTYPES:
         raise ValueError(f"out must be bfloat16, float16 or float32, got {out.dtype}")
     _need(out, "out", out.dtype, (T, N))
@@ -409,7 +409,7 @@ def _aligned_scales(scales, f):
     if (cols | scales.data_ptr()) % (16 if f else 8) == 0:
         return scales, cols
     rows, stride = scales.numel() // cols, (cols + 15) // 16 * 16
-    padded = torch.empty((rows, stride), dtype=torch.uint8, device=scales.device)
+    padded = scales.new_empty((rows, stride))
     _check(lib().moe_fp4_pad_scales(scales.data_ptr(), rows, cols, padded.data_ptr(), stride, _current(scales)),
            "moe_fp4_pad_scales")
     return padded, stride
@@ -424,7 +424,7 @@ def _fp4_product(f, x, x_scales, xss, x_ts, w, w_scales, w_ts, offsets, out, T, 
             x_scales, xss = _aligned_scales(x_scales, f)
     else:
         nbytes = L.moe_fp4_workspace_bytes(f, T, N, K, E)
-        space = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
+        space = w.new_empty(nbytes)
     p = _Fp4Product(f, T, N, K, E, _VALUE_DTYPES[out.dtype], x.data_ptr(), x_scales.data_ptr(), xss, x_ts,
                     w.data_ptr(), w_scales.data_ptr(), wss, w_ts, _addr(offsets), out.data_ptr(), _addr(space), nbytes,
                     _addr(status))
@@ -495,7 +495,7 @@ def fp4_linear(x: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor, fmt: st
                  offsets=offsets, out=out, status=status)
     # one workspace: the codes, then the scales in rows padded to 16 bytes (read in whole vectors)
     ss = (K // FP4_BLOCK[fmt] + 15) // 16 * 16
-    codes = torch.empty(T * (K // 2 + ss), dtype=torch.uint8, device=x.device)
+    codes = w.new_empty(T * (K // 2 + ss))
     scales = codes[T * (K // 2):]
     _check(lib().moe_quantize_fp4(f, x.data_ptr(), code, T, K, rs, x_ts, codes.data_ptr(), scales.data_ptr(), ss,
                                   _current(x)), "moe_quantize_fp4")

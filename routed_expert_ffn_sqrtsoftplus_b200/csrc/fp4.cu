@@ -44,73 +44,70 @@ __device__ __forceinline__ float value_f32(float v) { return v; }
 __device__ __forceinline__ float value_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ float value_f32(__half v) { return __half2float(v); }
 
-// 16 consecutive values and the largest magnitude among them; not finite: false. Magnitudes are
-// compared as integers, in which infinity and NaN come last, two 16-bit values at a time.
-__device__ __forceinline__ bool load16(const float* p, bool vec, float (&v)[kRun], float& amax) {
-  if (vec) {
+// 16 consecutive values as they are in memory.
+template <typename T>
+struct Raw {
+  static constexpr int kWords = kRun * sizeof(T) / 4;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void load(const T* p, bool vec) {
+    if (vec) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const float4 f = __ldg(reinterpret_cast<const float4*>(p) + q);
-      v[4 * q] = f.x;
-      v[4 * q + 1] = f.y;
-      v[4 * q + 2] = f.z;
-      v[4 * q + 3] = f.w;
+      for (int q = 0; q < kWords / 4; ++q) {
+        const uint4 u = __ldg(reinterpret_cast<const uint4*>(p) + q);
+        w[4 * q] = u.x;
+        w[4 * q + 1] = u.y;
+        w[4 * q + 2] = u.z;
+        w[4 * q + 3] = u.w;
+      }
+    } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t*>(p) + i);
+    } else {
+      const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
+#pragma unroll
+      for (int i = 0; i < kWords; ++i)
+        w[i] = static_cast<uint32_t>(__ldg(h + 2 * i)) | static_cast<uint32_t>(__ldg(h + 2 * i + 1)) << 16;
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < kRun; ++i) v[i] = __ldg(p + i);
   }
+};
+// The values in 32 bits and the largest magnitude among them; not finite: false. Magnitudes are compared
+// as integers, in which infinity and NaN come last, two 16-bit values at a time.
+__device__ __forceinline__ bool unpack(const Raw<float>& r, float (&v)[kRun], float& amax) {
   uint32_t m = 0u;
 #pragma unroll
-  for (int i = 0; i < kRun; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+  for (int i = 0; i < kRun; ++i) {
+    m = max(m, r.w[i] & 0x7FFFFFFFu);
+    v[i] = __uint_as_float(r.w[i]);
+  }
   amax = __uint_as_float(m);
   return m < 0x7F800000u;
 }
-template <typename T>
-__device__ __forceinline__ bool load16_half(const T* p, bool vec, uint32_t (&w)[8], uint32_t infinity, uint32_t& m) {
-  if (vec) {
+__device__ __forceinline__ uint32_t largest16(const uint32_t (&w)[8]) {
+  uint32_t m = 0u;
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const uint4 u = __ldg(reinterpret_cast<const uint4*>(p) + q);
-      w[4 * q] = u.x;
-      w[4 * q + 1] = u.y;
-      w[4 * q + 2] = u.z;
-      w[4 * q + 3] = u.w;
-    }
-  } else {
-    const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      w[i] = static_cast<uint32_t>(__ldg(h + 2 * i)) | static_cast<uint32_t>(__ldg(h + 2 * i + 1)) << 16;
-  }
-  uint32_t mm = 0u;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) mm = __vmaxu2(mm, w[i] & 0x7FFF7FFFu);
-  m = max(mm & 0xFFFFu, mm >> 16);
-  return m < infinity;
+  for (int i = 0; i < 8; ++i) m = __vmaxu2(m, w[i] & 0x7FFF7FFFu);
+  return max(m & 0xFFFFu, m >> 16);
 }
-__device__ __forceinline__ bool load16(const __nv_bfloat16* p, bool vec, float (&v)[kRun], float& amax) {
-  uint32_t w[8], m;
-  const bool finite = load16_half(p, vec, w, 0x7F80u, m);
+__device__ __forceinline__ bool unpack(const Raw<__nv_bfloat16>& r, float (&v)[kRun], float& amax) {
+  const uint32_t m = largest16(r.w);
   amax = __uint_as_float(m << 16);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    v[2 * i] = __uint_as_float(r.w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(r.w[i] & 0xFFFF0000u);
   }
-  return finite;
+  return m < 0x7F80u;
 }
-__device__ __forceinline__ bool load16(const __half* p, bool vec, float (&v)[kRun], float& amax) {
-  uint32_t w[8], m;
-  const bool finite = load16_half(p, vec, w, 0x7C00u, m);
+__device__ __forceinline__ bool unpack(const Raw<__half>& r, float (&v)[kRun], float& amax) {
+  const uint32_t m = largest16(r.w);
   amax = __half2float(__ushort_as_half(static_cast<unsigned short>(m)));
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&r.w[i]));
     v[2 * i] = f.x;
     v[2 * i + 1] = f.y;
   }
-  return finite;
+  return m < 0x7C00u;
 }
 
 // E4M3 value of a non-negative code (0 .. 126).
@@ -169,58 +166,74 @@ __device__ __forceinline__ uint32_t settle(uint32_t lo, uint32_t hi, const T* p,
   return lo;
 }
 
+// Runs a thread takes, a block's width apart and loaded together: two of 16-bit values to MXFP4, which
+// HBM bounds (8192 x 5120: 18.3 us against 21.9 with one); one to NVFP4, whose arithmetic bounds it (26
+// us either way), and of 32-bit values, for their registers.
+template <typename T, bool kNv>
+constexpr int kRuns = sizeof(T) == 4 || kNv ? 1 : 2;
+
 template <typename T, bool kNv>
 __global__ void __launch_bounds__(256)
     quantize_fp4_kernel(const T* __restrict__ src, uint32_t runs, FastDiv per_row, int64_t row_stride, int vec,
                         const float* __restrict__ tensor_scale, uint2* __restrict__ codes,
                         uint8_t* __restrict__ scales, int64_t scale_stride) {
-  const uint32_t i = blockIdx.x * 256u + threadIdx.x;
-  // cols % 32 == 0: an even number of runs, so that a lane and its neighbour are in range together
-  if (i >= runs) return;
-  const uint32_t row = divide(i, per_row);
-  const uint32_t run = i - row * per_row.d;
-  float v[kRun], amax;
-  bool finite = load16(src + row * row_stride + run * kRun, vec != 0, v, amax);
-  uint32_t w[2] = {0u, 0u};
-  if constexpr (!kNv) {
-    const unsigned pair = 3u << ((threadIdx.x & 31) & ~1);
-    // a block that is not finite is one as a whole: the larger magnitude, compared as an integer
-    const uint32_t m = max(__float_as_uint(amax), __shfl_xor_sync(pair, __float_as_uint(amax), 1));
-    finite = m < 0x7F800000u;
-    int code;
-    float inv;
-    mx_scale(__uint_as_float(m), 2, code, inv);
-    // a power of two: the products are exact, and the conversion rounds them as the format asks
-    w[0] = to_e2m1x8(v, inv);
-    w[1] = to_e2m1x8(v + 8, inv);
-    if (!finite) {
-      code = 0xFF;
-      w[0] = w[1] = 0u;
+  const uint32_t first = blockIdx.x * (256u * kRuns<T, kNv>) + threadIdx.x;
+  Raw<T> raw[kRuns<T, kNv>];
+#pragma unroll
+  for (int u = 0; u < kRuns<T, kNv>; ++u) {
+    const uint32_t i = first + 256u * u;
+    if (i < runs) {
+      const uint32_t row = divide(i, per_row);
+      raw[u].load(src + row * row_stride + (i - row * per_row.d) * kRun, vec != 0);
     }
-    if ((run & 1) == 0) scales[row * scale_stride + run / 2] = static_cast<uint8_t>(code);
-  } else {
-    const float ts = tensor_scale ? __ldg(tensor_scale) : 1.0f;
-    const int code = finite ? e4m3_scale(amax, ts) : 0x7F;
-    const float d = finite ? e4m3_value(code) * ts : 0.f;
-    const uint32_t db = __float_as_uint(d);
-    if (db >= 0x00800000u && db < 0x7F800000u) {  // a unit below the normal range counts as 0
-      // Quotients by two reciprocals, one a little low, one a little high: where both give the same
-      // codes, so does the exact quotient. (A unit that is a power of two divides exactly.)
-      const bool pow2 = (db & 0x7FFFFFu) == 0u && db >= 0x01000000u && db <= 0x7E000000u;
-      const float inv = pow2 ? __uint_as_float(0x7F000000u - db) : __fdividef(1.0f, d);
-      const float lo = pow2 ? inv : inv * (1.0f - 0x1p-20f), hi = pow2 ? inv : inv * (1.0f + 0x1p-20f);
-      w[0] = to_e2m1x8(v, lo);
-      w[1] = to_e2m1x8(v + 8, lo);
-      const uint32_t u0 = to_e2m1x8(v, hi), u1 = to_e2m1x8(v + 8, hi);
-      // Real tensors do come near borders: a tensor scale taken from a 16-bit maximum puts many blocks'
-      // units at simple fractions of their values (1.5 % of the runs of normally distributed rows).
-      const T* p = src + row * row_stride + run * kRun;
-      w[0] = settle(w[0], u0, p, d);
-      w[1] = settle(w[1], u1, p + 8, d);
-    }
-    scales[row * scale_stride + run] = static_cast<uint8_t>(code);
   }
-  codes[i] = make_uint2(w[0], w[1]);
+  const float ts = kNv && tensor_scale ? __ldg(tensor_scale) : 1.0f;
+#pragma unroll
+  for (int u = 0; u < kRuns<T, kNv>; ++u) {
+    const uint32_t i = first + 256u * u;
+    // cols % 32 == 0: an even number of runs, so that a lane and its neighbour are in range together
+    if (i >= runs) return;
+    const uint32_t row = divide(i, per_row);
+    const uint32_t run = i - row * per_row.d;
+    float v[kRun], amax;
+    bool finite = unpack(raw[u], v, amax);
+    uint32_t w[2] = {0u, 0u};
+    if constexpr (!kNv) {
+      const unsigned pair = 3u << ((threadIdx.x & 31) & ~1);
+      // a block that is not finite is one as a whole: the larger magnitude, compared as an integer
+      const uint32_t m = max(__float_as_uint(amax), __shfl_xor_sync(pair, __float_as_uint(amax), 1));
+      finite = m < 0x7F800000u;
+      int code;
+      float inv;
+      mx_scale(__uint_as_float(m), 2, code, inv);
+      // a power of two: the products are exact, and the conversion rounds them as the format asks
+      w[0] = to_e2m1x8(v, inv);
+      w[1] = to_e2m1x8(v + 8, inv);
+      if (!finite) {
+        code = 0xFF;
+        w[0] = w[1] = 0u;
+      }
+      if ((run & 1) == 0) scales[row * scale_stride + run / 2] = static_cast<uint8_t>(code);
+    } else {
+      const int code = finite ? e4m3_scale(amax, ts) : 0x7F;
+      const float d = finite ? e4m3_value(code) * ts : 0.f;
+      const uint32_t db = __float_as_uint(d);
+      if (db >= 0x00800000u && db < 0x7F800000u) {  // a unit below the normal range counts as 0
+        // Quotients by two reciprocals, one a little low, one a little high: where both give the same
+        // codes, so does the exact quotient. (A unit that is a power of two divides exactly.)
+        const bool pow2 = (db & 0x7FFFFFu) == 0u && db >= 0x01000000u && db <= 0x7E000000u;
+        const float inv = pow2 ? __uint_as_float(0x7F000000u - db) : __fdividef(1.0f, d);
+        const float lo = pow2 ? inv : inv * (1.0f - 0x1p-20f), hi = pow2 ? inv : inv * (1.0f + 0x1p-20f);
+        // Real tensors do come near borders: a tensor scale taken from a 16-bit maximum puts many blocks'
+        // units at simple fractions of their values (1.5 % of the runs of normally distributed rows).
+        const T* p = src + row * row_stride + run * kRun;
+        w[0] = settle(to_e2m1x8(v, lo), to_e2m1x8(v, hi), p, d);
+        w[1] = settle(to_e2m1x8(v + 8, lo), to_e2m1x8(v + 8, hi), p + 8, d);
+      }
+      scales[row * scale_stride + run] = static_cast<uint8_t>(code);
+    }
+    codes[i] = make_uint2(w[0], w[1]);
+  }
 }
 
 // Eight consecutive values.
@@ -327,7 +340,7 @@ cudaError_t quantize_t(const void* src, int64_t rows, int cols, int64_t row_stri
                        uint8_t* scales, int64_t scale_stride, cudaStream_t s) {
   const uint32_t rpr = cols / kRun, runs = static_cast<uint32_t>(rows * rpr);
   const bool vec = reinterpret_cast<uintptr_t>(src) % 16 == 0 && (row_stride * sizeof(T)) % 16 == 0;
-  quantize_fp4_kernel<T, kNv><<<(runs + 255) / 256, 256, 0, s>>>(
+  quantize_fp4_kernel<T, kNv><<<(runs + 256 * kRuns<T, kNv> - 1) / (256 * kRuns<T, kNv>), 256, 0, s>>>(
       static_cast<const T*>(src), runs, fast_div(rpr), row_stride, vec ? 1 : 0, ts, reinterpret_cast<uint2*>(codes), scales,
       scale_stride);
   return cudaGetLastError();

@@ -16,9 +16,14 @@
 //
 // Exactness. Without a bias the three scores grow with the logit, so the logits
 // themselves are the keys and the selection is exact. With a bias, or where a group is
-// worth the sum of two scores, keys are 32-bit sums with an error below kKeyTol; a row
-// in which two neighbours of the selection are nearer than that is selected again from
-// 64-bit keys (select_row_f64), so the result is always that of the 64-bit keys.
+// worth the sum of two scores, keys are 32-bit sums with a small error (key_tol). Where
+// two neighbours of a row's selection are nearer than that, the experts that may belong
+// to it, one per lane, are put in order by 64-bit keys (order_f64); where it is the groups
+// that cannot be told apart, the experts that may count in their worth are (groups_f64). A row
+// with more than 32 of either is selected from 64-bit keys as a whole (select_row_f64). So the
+// result is always that of the 64-bit keys.
+//
+// Bound by the selection's instructions: some 550 a row, where the row is 1 KB.
 #include <cuda_fp16.h>
 
 #include "common.cuh"
@@ -31,10 +36,13 @@ namespace {
 constexpr int kRouteWarps = 4;  // rows per block
 constexpr uint32_t kFull = 0xffffffffu;
 
-// 32-bit keys against exact ones, relative to 1 + |key|: the scores' exp, log and divide
-// are good to a few units of 2^-24 and s * |z - max| (softmax) stays below 1/e; the sum
-// with the bias rounds once more. 2^-20 covers both neighbours with a factor to spare.
-constexpr float kKeyTol = 9.5367431640625e-7f;
+// Two 32-bit keys may stand in the wrong order where they are no further apart than this, times 1 + |key|.
+// Sigmoid: __expf is off by 2 + 1.2 |x| units of 2^-23, of which u / (1 + u)^2 (at most 0.6 units in all)
+// reaches the score; the quotient, 1 + u and the sum with the bias add two: below 2^-21 a key. The terms of
+// sqrt(log(1 + e^z)) are good to a unit each. Softmax: the sum of up to 512 terms adds up to 21 roundings.
+__device__ __forceinline__ float key_tol(int score) {
+  return score == kScoreSoftmax ? 3.814697265625e-6f : 9.5367431640625e-7f;  // 2^-18, 2^-20
+}
 
 template <typename T>
 __device__ __forceinline__ float to_f32(T v);
@@ -122,6 +130,14 @@ __device__ __forceinline__ float score_f32(float z, int score, float m, float in
   if (score == kScoreSigmoid) return sigmoid_f32(z);
   return sqrtf(fmaxf(z, 0.0f) + log1pf(expf(-fabsf(z))));
 }
+// The same for keys.
+__device__ __forceinline__ float key_score(float z, int score, float m, float inv_sum) {
+  if (score == kScoreSigmoid) {
+    const float u = __expf(-fabsf(z));
+    return __fdividef(z >= 0.0f ? 1.0f : u, 1.0f + u);
+  }
+  return score_f32(z, score, m, inv_sum);
+}
 __device__ __forceinline__ double score_f64(double z, int score, double m, double sum) {
   if (score == kScoreSoftmax) return exp(z - m) / sum;
   if (score == kScoreSigmoid) {
@@ -149,16 +165,87 @@ struct SelectArgs {
   int E, G, kept, k, score, sum2;
 };
 
+// Maximum and sum of a softmax row in 64 bits.
+template <typename T>
+__device__ __forceinline__ void softmax_f64(const T* row, int E, int lane, double& m, double& sum) {
+  m = -INFINITY;
+  sum = 0.0;
+  for (int e = lane; e < E; e += 32) m = fmax(m, static_cast<double>(to_f32<T>(row[e])));
+  for (int o = 16; o > 0; o >>= 1) m = fmax(m, __shfl_xor_sync(kFull, m, o));
+  for (int e = lane; e < E; e += 32) sum += exp(static_cast<double>(to_f32<T>(row[e])) - m);
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+}
+
+// The experts of lanes 0 .. n - 1 in the order of their 64-bit keys: lane r gets the r-th, or -1.
+template <typename T>
+__device__ __noinline__ int order_f64(const T* row, const float* bias, int E, int score, int cand, int n, int lane) {
+  double m = 0.0, sum = 1.0;
+  if (score == kScoreSoftmax) softmax_f64<T>(row, E, lane, m, sum);
+  const bool has = lane < n;
+  const double key = has ? score_f64(static_cast<double>(to_f32<T>(row[cand])), score, m, sum) +
+                               (bias ? static_cast<double>(bias[cand]) : 0.0)
+                         : -INFINITY;
+  int rank = 0;
+#pragma unroll 4
+  for (int j = 0; j < n; ++j) {
+    const double o = __shfl_sync(kFull, key, j);
+    const int oc = __shfl_sync(kFull, cand, j);
+    rank += o > key || (o == key && oc < cand);
+  }
+  int mine = -1;
+#pragma unroll 4
+  for (int j = 0; j < n; ++j) {
+    const int oc = __shfl_sync(kFull, cand, j), orank = __shfl_sync(kFull, rank, j);
+    if (orank == lane) mine = oc;
+  }
+  return mine;
+}
+
+// The kept groups (a mask) by the 64-bit keys of the experts of lanes 0 .. n - 1, which hold every group's
+// largest two.
+template <typename T>
+__device__ __noinline__ uint32_t groups_f64(const T* row, const float* bias, SelectArgs a, int cand, int n, int lane) {
+  double m = 0.0, sum = 1.0;
+  if (a.score == kScoreSoftmax) softmax_f64<T>(row, a.E, lane, m, sum);
+  const bool has = lane < n;
+  const double key = has ? score_f64(static_cast<double>(to_f32<T>(row[cand])), a.score, m, sum) +
+                               (bias ? static_cast<double>(bias[cand]) : 0.0)
+                         : -INFINITY;
+  const int group = has ? cand / (a.E / a.G) : -1;
+  double w1 = -INFINITY, w2 = -INFINITY;
+#pragma unroll 4
+  for (int j = 0; j < n; ++j) {
+    const double o = __shfl_sync(kFull, key, j);
+    if (__shfl_sync(kFull, group, j) == lane) {
+      w2 = fmax(w2, fmin(w1, o));
+      w1 = fmax(w1, o);
+    }
+  }
+  const double worth = a.sum2 && w2 != -INFINITY ? w1 + w2 : w1;
+  int rank = 0;
+  for (int g = 0; g < a.G; ++g) {
+    const double o = __shfl_sync(kFull, worth, g);
+    rank += o > worth || (o == worth && g < lane);
+  }
+  return __ballot_sync(kFull, lane < a.G && rank < a.kept);
+}
+
+// The j-th (from 0) of a warp's flags gathered so far: which of its elements a lane takes.
+struct Gather {
+  int cand = -1, total = 0;
+  __device__ __forceinline__ void add(bool in, int lane, int epl, int i) {
+    const uint32_t who = __ballot_sync(kFull, in);
+    const int at = lane - total;
+    if (at >= 0 && at < __popc(who)) cand = static_cast<int>(__fns(who, 0, at + 1)) * epl + i;
+    total += __popc(who);
+  }
+};
+
 // The selection from 64-bit keys held in `buf` (E doubles): lane r < k gets slot r's expert or -1.
 template <typename T>
 __device__ __noinline__ int select_row_f64(const T* row, const float* bias, SelectArgs a, double* buf, int lane) {
-  double m = -INFINITY, sum = 0.0;
-  if (a.score == kScoreSoftmax) {
-    for (int e = lane; e < a.E; e += 32) m = fmax(m, static_cast<double>(to_f32<T>(row[e])));
-    for (int o = 16; o > 0; o >>= 1) m = fmax(m, __shfl_xor_sync(kFull, m, o));
-    for (int e = lane; e < a.E; e += 32) sum += exp(static_cast<double>(to_f32<T>(row[e])) - m);
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
-  }
+  double m = 0.0, sum = 1.0;
+  if (a.score == kScoreSoftmax) softmax_f64<T>(row, a.E, lane, m, sum);
   for (int e = lane; e < a.E; e += 32) {
     const double z = to_f32<T>(row[e]);
     buf[e] = z == -INFINITY ? -INFINITY
@@ -215,7 +302,7 @@ __device__ __noinline__ int select_row_f64(const T* row, const float* bias, Sele
 template <typename T, int EPL>
 __global__ void __launch_bounds__(kRouteWarps * 32)
     route_kernel(const T* __restrict__ logits, int64_t row_stride, const float* __restrict__ bias, int rows,
-                 SelectArgs a, int renorm, float scale, int vec, int32_t* __restrict__ idx_out,
+                 SelectArgs a, int renorm, float scale, int vec, int vec_bias, int32_t* __restrict__ idx_out,
                  float* __restrict__ w_out) {
   extern __shared__ double key_buf[];  // E doubles per warp, where keys are sums
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -235,6 +322,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
   }
   const bool grouped = a.kept < a.G;
   const bool need_scores = bias != nullptr || (grouped && a.sum2);
+  const float tol = key_tol(a.score);
   float inv_sum = 1.0f;
   if (a.score == kScoreSoftmax) {
     zmax = warp_max(zmax);
@@ -248,13 +336,15 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
   // keys: the scores plus bias where there is one (v), else the logits
   uint32_t key[EPL];
   float v[EPL];
+  if (bias != nullptr) load_run<float, EPL>(bias + e0, min(EPL, a.E - e0), vec_bias != 0, v);
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
     const bool live = z[i] != -INFINITY;
+    const float b = bias != nullptr ? v[i] : 0.f;
     v[i] = z[i];
-    if (need_scores && live) v[i] = score_f32(z[i], a.score, zmax, inv_sum);
+    if (need_scores && live) v[i] = key_score(z[i], a.score, zmax, inv_sum);
     if (bias != nullptr && live) {
-      v[i] += __ldg(bias + e0 + i);
+      v[i] += b;
       bad |= !(fabsf(v[i]) < INFINITY);
     }
     key[i] = live ? key_of(bias != nullptr ? v[i] : z[i]) : 0u;
@@ -312,17 +402,34 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
       rank += o > worth || (o == worth && g < lane);
     }
     const bool in = lane < a.G && rank < a.kept;
-    const uint32_t keep = __ballot_sync(kFull, in);
+    uint32_t keep = __ballot_sync(kFull, in);
     if (need_scores) {
       // the least of the kept and the best of the others
       const float least = -warp_max(in ? -worth : -INFINITY);
       const float best = warp_max(in ? -INFINITY : worth);
-      unsure = best != -INFINITY && least - best <= 4.0f * kKeyTol * (1.0f + fabsf(best));
+      if (best != -INFINITY && least - best <= 2.0f * tol * (1.0f + fabsf(best))) {
+        // of each group, what reaches its second (or its first) key
+        const float low = a.sum2 && w2 != -INFINITY ? w2 : w1;
+        const float from = lane < a.G ? low - tol * (1.0f + fabsf(low)) : INFINITY;
+        Gather cands;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+          const float f = __shfl_sync(kFull, from, min(e0 + i, a.E - 1) / Eg);
+          cands.add(v[i] != -INFINITY && v[i] >= f, lane, EPL, i);
+        }
+        if (cands.total <= 32)
+          keep = groups_f64<T>(row, bias, a, cands.cand, cands.total, lane);
+        else
+          unsure = true;
+      }
     }
     int g = e0 / Eg, left = Eg - e0 % Eg;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-      if (e0 + i < a.E && !((keep >> g) & 1u)) key[i] = 0u;
+      if (e0 + i < a.E && !((keep >> g) & 1u)) {
+        key[i] = 0u;
+        v[i] = -INFINITY;
+      }
       if (--left == 0) {
         ++g;
         left = Eg;
@@ -338,22 +445,18 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
       bk = key[i];
       bi = i;
     }
-  int mine = -1;
-  uint32_t last = 0u;
-  for (int r = 0;; ++r) {
+  int mine = -1, n = 0;
+  uint32_t mkey = 0u;  // slot `lane`'s key; slot k's is the best one left
+  for (; n <= a.k; ++n) {
     const uint32_t m = __reduce_max_sync(kFull, bk);
-    if (bias != nullptr && r > 0 && m != 0u) {
-      const float hi = value_of(last);
-      unsure |= hi - value_of(m) <= 2.0f * kKeyTol * (1.0f + fabsf(hi));
-    }
-    if (r == a.k || m == 0u) break;
-    last = m;
+    if (lane == n) mkey = m;
+    if (n == a.k || m == 0u) break;
     const int win = __ffs(__ballot_sync(kFull, bk == m)) - 1;
     const int e = __shfl_sync(kFull, e0 + bi, win);
-    if (lane == r) mine = e;
+    if (lane == n) mine = e;
     if (lane == win) {
-      bk = 0u;
       const int was = bi;
+      bk = 0u;
 #pragma unroll
       for (int i = 0; i < EPL; ++i) {
         if (i == was) key[i] = 0u;
@@ -362,6 +465,24 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
           bi = i;
         }
       }
+    }
+  }
+  if (bias != nullptr) {
+    // neighbours that 32-bit keys do not tell apart: order what reaches down to the last slot's key again
+    const float mine_f = value_of(mkey), up = __shfl_up_sync(kFull, mine_f, 1);
+    const bool close = lane > 0 && lane <= n && mkey != 0u && up - mine_f <= tol * (1.0f + fabsf(up));
+    if (!unsure && __any_sync(kFull, close)) {
+      const float last = __shfl_sync(kFull, mine_f, n - 1);
+      const float least = last - tol * (1.0f + fabsf(last));
+      Gather cands;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i)  // with a bias v holds the keys, -infinity where the expert is out
+        cands.add(v[i] != -INFINITY && v[i] >= least, lane, EPL, i);
+      if (cands.total <= 32)
+        mine = order_f64<T>(row, bias, a.E, a.score, cands.cand, cands.total, lane);
+      else
+        unsure = true;
+      if (lane >= a.k) mine = -1;
     }
   }
   if (unsure) mine = select_row_f64<T>(row, bias, a, key_buf + static_cast<size_t>(warp) * a.E, lane);
@@ -501,7 +622,8 @@ cudaError_t launch_route_epl(const RouteArgs& r, cudaStream_t s) {
   const size_t smem = need ? static_cast<size_t>(kRouteWarps) * r.E * sizeof(double) : 0;
   const SelectArgs a{r.E, r.n_groups, r.topk_groups, r.k, r.score, r.group_sum2};
   route_kernel<T, EPL><<<(r.T + kRouteWarps - 1) / kRouteWarps, kRouteWarps * 32, smem, s>>>(
-      static_cast<const T*>(r.logits), r.row_stride, r.bias, r.T, a, r.renorm, r.scale, vec ? 1 : 0, r.idx, r.w);
+      static_cast<const T*>(r.logits), r.row_stride, r.bias, r.T, a, r.renorm, r.scale, vec ? 1 : 0,
+      reinterpret_cast<uintptr_t>(r.bias) % 16 == 0 ? 1 : 0, r.idx, r.w);
   return cudaGetLastError();
 }
 
