@@ -11,8 +11,7 @@
 //
 // One warp per row: the row is read once and kept in registers, lane l holding the
 // consecutive experts l * EPL + i, so the lowest expert of a tie sits in the lowest
-// lane. The selection takes k rounds of a warp maximum over order-preserving 32-bit
-// keys (redux.sync).
+// lane. The selection works on order-preserving 32-bit keys (select_by_list).
 //
 // Exactness. Without a bias the three scores grow with the logit, so the logits
 // themselves are the keys and the selection is exact. With a bias, or where a group is
@@ -163,6 +162,8 @@ __device__ __forceinline__ float shared_score(float z, int score, float m) {
 
 struct SelectArgs {
   int E, G, kept, k, score, sum2;
+  int Eg;          // experts of a group
+  int lane_shift;  // a group is 2^lane_shift whole lanes, or -1
 };
 
 // Maximum and sum of a softmax row in 64 bits.
@@ -299,12 +300,106 @@ __device__ __noinline__ int select_row_f64(const T* row, const float* bias, Sele
   return mine;
 }
 
+// The k largest of the warp's keys (0: none) in order, lower expert first on a tie: lane r gets the r-th
+// expert and key, lane k the largest key left (0 if there is none); how many there are is returned.
+//
+// In rounds: a warp maximum (redux.sync) finds the next, and its lane looks for its next one.
+template <int EPL>
+__device__ __forceinline__ int select_by_rounds(uint32_t (&key)[EPL], int e0, int k, int lane, int& mine,
+                                                uint32_t& mkey) {
+  uint32_t bk = 0u;
+  int bi = 0, n = 0;
+#pragma unroll
+  for (int i = 0; i < EPL; ++i)
+    if (key[i] > bk) {
+      bk = key[i];
+      bi = i;
+    }
+#pragma unroll 1
+  for (; n <= k; ++n) {
+    const uint32_t m = __reduce_max_sync(kFull, bk);
+    if (lane == n) mkey = m;
+    if (n == k || m == 0u) break;
+    const int win = __ffs(__ballot_sync(kFull, bk == m)) - 1;
+    const int e = __shfl_sync(kFull, e0 + bi, win);
+    if (lane == n) mine = e;
+    if (lane == win) {
+      const int was = bi;
+      bk = 0u;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        if (i == was) key[i] = 0u;
+        if (key[i] > bk) {
+          bk = key[i];
+          bi = i;
+        }
+      }
+    }
+  }
+  return n;
+}
+
+// By a list: the k-th largest of the lanes' maxima bounds the k-th largest key from below, and few keys
+// reach that bound. They go to a list of at most 32 (key, expert), one a lane, and each counts those ahead of
+// it. -1 where there are more (many equal keys); `tol` lowers the bound, so that the list also holds what
+// floats cannot tell from the last slot. Some 200 instructions where rounds take 60 each.
+constexpr int kListK = 12;  // above, the bound lets too many through
+template <int EPL>
+__device__ __forceinline__ int select_by_list(const uint32_t (&key)[EPL], int e0, int k, float tol, uint2* list,
+                                              int lane, int& mine, uint32_t& mkey) {
+  uint32_t bk = 0u;
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) bk = max(bk, key[i]);
+  uint32_t bound = 0u;
+  int reached = 0;
+  for (int r = 0; r < k && reached < k; ++r) {  // equal maxima go together
+    bound = __reduce_max_sync(kFull, bk);
+    const bool top = bk == bound;
+    reached += __popc(__ballot_sync(kFull, top));
+    if (top) bk = 0u;
+  }
+  // fewer than k lanes with live experts: everything live
+  if (reached < k || bound == 0u) bound = 1u;
+  if (tol > 0.f && bound > 1u) {
+    const float f = value_of(bound);
+    bound = max(1u, key_of(f - tol * (1.0f + fabsf(f))));
+  }
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    const bool in = key[i] >= bound;
+    const uint32_t who = __ballot_sync(kFull, in);
+    const int at = n + __popc(who & ((1u << lane) - 1u));
+    if (in && at < 32) list[at] = make_uint2(key[i], static_cast<uint32_t>(e0 + i));
+    n += __popc(who);
+  }
+  if (n > 32) return -1;
+  __syncwarp();
+  const uint2 my = lane < n ? list[lane] : make_uint2(0u, 0x7FFFFFFFu);
+  int rank = 0;
+#pragma unroll 4
+  for (int j = 0; j < n; ++j) {
+    const uint2 o = list[j];
+    rank += o.x > my.x || (o.x == my.x && o.y < my.y);
+  }
+  __syncwarp();
+  if (lane < n) list[rank] = my;
+  __syncwarp();
+  if (lane < n && lane <= k) {
+    const uint2 o = list[lane];
+    mkey = o.x;
+    if (lane < k) mine = static_cast<int>(o.y);
+  }
+  return min(n, k);
+}
+
 template <typename T, int EPL>
 __global__ void __launch_bounds__(kRouteWarps * 32)
     route_kernel(const T* __restrict__ logits, int64_t row_stride, const float* __restrict__ bias, int rows,
                  SelectArgs a, int renorm, float scale, int vec, int vec_bias, int32_t* __restrict__ idx_out,
                  float* __restrict__ w_out) {
   extern __shared__ double key_buf[];  // E doubles per warp, where keys are sums
+  __shared__ uint2 list_buf[kRouteWarps][32];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int t = blockIdx.x * kRouteWarps + warp;
   if (t >= rows) return;
@@ -359,22 +454,23 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
 
   bool unsure = false;  // two neighbours of a choice nearer than 32-bit keys tell
   if (grouped) {
-    const int Eg = a.E / a.G;
+    const int Eg = a.Eg;
+    // a group is a power of two of whole lanes: 2^lane_shift of them
+    const bool whole = a.lane_shift >= 0;
     float w1 = -INFINITY, w2 = -INFINITY;
-    if (Eg % EPL == 0 && ((Eg / EPL) & (Eg / EPL - 1)) == 0 && Eg / EPL <= 32) {
-      // a group is a power of two of whole lanes: merge the lanes' two largest
+    if (whole) {
+      // merge the lanes' two largest
 #pragma unroll
       for (int i = 0; i < EPL; ++i) {
         w2 = fmaxf(w2, fminf(w1, v[i]));
         w1 = fmaxf(w1, v[i]);
       }
-      const int lanes = Eg / EPL;
-      for (int o = 1; o < lanes; o <<= 1) {
+      for (int o = 1; o < 1 << a.lane_shift; o <<= 1) {
         const float o1 = __shfl_xor_sync(kFull, w1, o), o2 = __shfl_xor_sync(kFull, w2, o);
         w2 = fmaxf(fmaxf(w2, o2), fminf(w1, o1));
         w1 = fmaxf(w1, o1);
       }
-      const int src = min(lane, a.G - 1) * lanes;  // lane g takes group g's
+      const int src = min(lane, a.G - 1) << a.lane_shift;  // lane g takes group g's
       w1 = __shfl_sync(kFull, w1, src);
       w2 = __shfl_sync(kFull, w2, src);
     } else {
@@ -397,6 +493,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
     float worth = a.sum2 && w2 != -INFINITY ? w1 + w2 : w1;
     if (lane >= a.G) worth = -INFINITY;
     int rank = 0;
+#pragma unroll 4
     for (int g = 0; g < a.G; ++g) {
       const float o = __shfl_sync(kFull, worth, g);
       rank += o > worth || (o == worth && g < lane);
@@ -404,10 +501,11 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
     const bool in = lane < a.G && rank < a.kept;
     uint32_t keep = __ballot_sync(kFull, in);
     if (need_scores) {
-      // the least of the kept and the best of the others
-      const float least = -warp_max(in ? -worth : -INFINITY);
-      const float best = warp_max(in ? -INFINITY : worth);
-      if (best != -INFINITY && least - best <= 2.0f * tol * (1.0f + fabsf(best))) {
+      // the least of the kept and the best of the others, which lie side by side in the order
+      const float least = value_of(__reduce_min_sync(kFull, in ? key_of(worth) : kFull));
+      const uint32_t best_key = __reduce_max_sync(kFull, in || worth == -INFINITY ? 0u : key_of(worth));
+      const float best = value_of(best_key);
+      if (best_key != 0u && least - best <= 2.0f * tol * (1.0f + fabsf(best))) {
         // of each group, what reaches its second (or its first) key
         const float low = a.sum2 && w2 != -INFINITY ? w2 : w1;
         const float from = lane < a.G ? low - tol * (1.0f + fabsf(low)) : INFINITY;
@@ -423,50 +521,34 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
           unsure = true;
       }
     }
-    int g = e0 / Eg, left = Eg - e0 % Eg;
+    if (whole) {
+      const bool out = !((keep >> (lane >> a.lane_shift)) & 1u);
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      if (e0 + i < a.E && !((keep >> g) & 1u)) {
-        key[i] = 0u;
-        v[i] = -INFINITY;
-      }
-      if (--left == 0) {
-        ++g;
-        left = Eg;
-      }
-    }
-  }
-
-  uint32_t bk = 0u;
-  int bi = 0;
-#pragma unroll
-  for (int i = 0; i < EPL; ++i)
-    if (key[i] > bk) {
-      bk = key[i];
-      bi = i;
-    }
-  int mine = -1, n = 0;
-  uint32_t mkey = 0u;  // slot `lane`'s key; slot k's is the best one left
-  for (; n <= a.k; ++n) {
-    const uint32_t m = __reduce_max_sync(kFull, bk);
-    if (lane == n) mkey = m;
-    if (n == a.k || m == 0u) break;
-    const int win = __ffs(__ballot_sync(kFull, bk == m)) - 1;
-    const int e = __shfl_sync(kFull, e0 + bi, win);
-    if (lane == n) mine = e;
-    if (lane == win) {
-      const int was = bi;
-      bk = 0u;
+      for (int i = 0; i < EPL; ++i)
+        if (out) {
+          key[i] = 0u;
+          v[i] = -INFINITY;
+        }
+    } else {
+      int g = e0 / Eg, left = Eg - e0 % Eg;
 #pragma unroll
       for (int i = 0; i < EPL; ++i) {
-        if (i == was) key[i] = 0u;
-        if (key[i] > bk) {
-          bk = key[i];
-          bi = i;
+        if (e0 + i < a.E && !((keep >> g) & 1u)) {
+          key[i] = 0u;
+          v[i] = -INFINITY;
+        }
+        if (--left == 0) {
+          ++g;
+          left = Eg;
         }
       }
     }
   }
+
+  int mine = -1, n = 0;  // slot `lane`'s expert; slots filled
+  uint32_t mkey = 0u;    // its key; slot k's is the best one left
+  if (a.k <= kListK) n = select_by_list<EPL>(key, e0, a.k, bias != nullptr ? tol : 0.f, list_buf[warp], lane, mine, mkey);
+  if (a.k > kListK || n < 0) n = select_by_rounds<EPL>(key, e0, a.k, lane, mine, mkey);
   if (bias != nullptr) {
     // neighbours that 32-bit keys do not tell apart: order what reaches down to the last slot's key again
     const float mine_f = value_of(mkey), up = __shfl_up_sync(kFull, mine_f, 1);
@@ -620,7 +702,11 @@ cudaError_t launch_route_epl(const RouteArgs& r, cudaStream_t s) {
   // 64-bit keys of the rows that need them, and the groups' keys where lanes do not align with groups
   const bool need = grouped || r.bias != nullptr;
   const size_t smem = need ? static_cast<size_t>(kRouteWarps) * r.E * sizeof(double) : 0;
-  const SelectArgs a{r.E, r.n_groups, r.topk_groups, r.k, r.score, r.group_sum2};
+  const int Eg = r.E / r.n_groups, lanes = Eg / EPL;
+  int shift = -1;
+  if (Eg % EPL == 0 && (lanes & (lanes - 1)) == 0)
+    for (shift = 0; 1 << shift < lanes;) ++shift;
+  const SelectArgs a{r.E, r.n_groups, r.topk_groups, r.k, r.score, r.group_sum2, Eg, shift};
   route_kernel<T, EPL><<<(r.T + kRouteWarps - 1) / kRouteWarps, kRouteWarps * 32, smem, s>>>(
       static_cast<const T*>(r.logits), r.row_stride, r.bias, r.T, a, r.renorm, r.scale, vec ? 1 : 0,
       reinterpret_cast<uintptr_t>(r.bias) % 16 == 0 ? 1 : 0, r.idx, r.w);
