@@ -550,7 +550,7 @@ typedef struct {
   int32_t format; /* moe_fp4_format */
   int32_t T, N, K, E;
   int32_t out_dtype;
-  const uint8_t* x;
+  const void* x; /* uint8 codes */
   const uint8_t* x_scales;
   int64_t x_scale_stride;
   const float* x_tensor_scale;
@@ -574,6 +574,15 @@ MOE_API moe_status moe_fp4_pad_scales(const uint8_t* src, int64_t rows, int32_t 
 MOE_API int64_t moe_fp4_workspace_bytes(int32_t format, int32_t T, int32_t N, int32_t K, int32_t E);
 
 MOE_API moe_status moe_fp4_matmul(const moe_fp4_product* p, moe_stream_t stream);
+
+/*
+ * The same with x [T, K] in x_dtype (moe_value_dtype), rows x_row_stride elements apart, quantised
+ * first (moe_quantize_fp4 with x_tensor_scale): p->x is x, p->x_scales and p->x_scale_stride are
+ * not used, and the workspace has moe_fp4_linear_workspace_bytes(...) bytes (never 0 for T > 0).
+ */
+MOE_API int64_t moe_fp4_linear_workspace_bytes(int32_t format, int32_t T, int32_t N, int32_t K, int32_t E);
+MOE_API moe_status moe_fp4_linear(const moe_fp4_product* p, int32_t x_dtype, int64_t x_row_stride,
+                                  moe_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -14,6 +14,7 @@ or no CUDA device is present the calls raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 from typing import Optional
@@ -37,7 +38,8 @@ EXPORTED = ("moe_create", "moe_forward", "moe_forward_host", "moe_get_status", "
             "moe_set_hash_table", "moe_forward_hashed", "moe_fill_workspace", "moe_create_ep",
             "moe_forward_partial", "moe_read_bandwidth", "moe_forward_host_async", "moe_forward_host_wait",
             "moe_route", "moe_route_backward", "moe_forward_routed", "moe_quantize_fp4", "moe_dequantize_fp4",
-            "moe_fp4_pad_scales", "moe_fp4_workspace_bytes", "moe_fp4_matmul")
+            "moe_fp4_pad_scales", "moe_fp4_workspace_bytes", "moe_fp4_matmul",
+            "moe_fp4_linear_workspace_bytes", "moe_fp4_linear")
 
 SCORES = {"softmax": 0, "sigmoid": 1, "sqrtsoftplus": 2}
 FP4_FORMATS = {"mxfp4": 0, "nvfp4": 1}
@@ -131,6 +133,8 @@ def lib() -> ctypes.CDLL:
             "moe_fp4_pad_scales": (I32, [P, I64, I32, P, I64, P]),
             "moe_fp4_workspace_bytes": (I64, [I32, I32, I32, I32, I32]),
             "moe_fp4_matmul": (I32, [ctypes.POINTER(_Fp4Product), P]),
+            "moe_fp4_linear_workspace_bytes": (I64, [I32, I32, I32, I32, I32]),
+            "moe_fp4_linear": (I32, [ctypes.POINTER(_Fp4Product), I32, I64, P]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -415,21 +419,10 @@ def _aligned_scales(scales, f):
     return padded, stride
 
 
-def _fp4_product(f, x, x_scales, xss, x_ts, w, w_scales, w_ts, offsets, out, T, N, K, E, status):
+@functools.lru_cache(maxsize=4096)
+def _fp4_workspace_bytes(linear, *shape):
     L = lib()
-    wss, space, nbytes = w_scales.shape[-1], None, 0
-    if T <= 32 * E:       # few rows: no workspace, but aligned rows of scales
-        w_scales, wss = _aligned_scales(w_scales, f)
-        if xss == x_scales.shape[-1]:
-            x_scales, xss = _aligned_scales(x_scales, f)
-    else:
-        nbytes = L.moe_fp4_workspace_bytes(f, T, N, K, E)
-        space = w.new_empty(nbytes)
-    p = _Fp4Product(f, T, N, K, E, _VALUE_DTYPES[out.dtype], x.data_ptr(), x_scales.data_ptr(), xss, x_ts,
-                    w.data_ptr(), w_scales.data_ptr(), wss, w_ts, _addr(offsets), out.data_ptr(), _addr(space), nbytes,
-                    _addr(status))
-    _check(L.moe_fp4_matmul(p, _current(x)), "moe_fp4_matmul")
-    return out
+    return (L.moe_fp4_linear_workspace_bytes if linear else L.moe_fp4_workspace_bytes)(*shape)
 
 
 def fp4_matmul(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor, fmt: str, *,
@@ -466,7 +459,17 @@ def fp4_matmul(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_scale
         _need(status, "status", torch.int32, (1,))
     _same_device(x, x_scales=x_scales, w=w, w_scales=w_scales, x_tensor_scale=x_tensor_scale,
                  w_tensor_scale=w_tensor_scale, offsets=offsets, out=out, status=status)
-    return _fp4_product(f, x, x_scales, x_scales.shape[1], x_ts, w, w_scales, w_ts, offsets, out, T, N, K, E, status)
+    xss, wss = x_scales.shape[1], w_scales.shape[-1]
+    if T <= 32 * E:       # few rows: no workspace, but aligned rows of scales
+        w_scales, wss = _aligned_scales(w_scales, f)
+        x_scales, xss = _aligned_scales(x_scales, f)
+    nbytes = _fp4_workspace_bytes(False, f, T, N, K, E)
+    space = w.new_empty(nbytes)
+    p = _Fp4Product(f, T, N, K, E, _VALUE_DTYPES[out.dtype], x.data_ptr(), x_scales.data_ptr(), xss, x_ts,
+                    w.data_ptr(), w_scales.data_ptr(), wss, w_ts, _addr(offsets), out.data_ptr(),
+                    space.data_ptr() if nbytes else None, nbytes, _addr(status))
+    _check(lib().moe_fp4_matmul(p, _current(x)), "moe_fp4_matmul")
+    return out
 
 
 def fp4_linear(x: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor, fmt: str, *,
@@ -493,13 +496,16 @@ def fp4_linear(x: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor, fmt: st
         _need(status, "status", torch.int32, (1,))
     _same_device(x, w=w, w_scales=w_scales, x_tensor_scale=x_tensor_scale, w_tensor_scale=w_tensor_scale,
                  offsets=offsets, out=out, status=status)
-    # one workspace: the codes, then the scales in rows padded to 16 bytes (read in whole vectors)
-    ss = (K // FP4_BLOCK[fmt] + 15) // 16 * 16
-    codes = w.new_empty(T * (K // 2 + ss))
-    scales = codes[T * (K // 2):]
-    _check(lib().moe_quantize_fp4(f, x.data_ptr(), code, T, K, rs, x_ts, codes.data_ptr(), scales.data_ptr(), ss,
-                                  _current(x)), "moe_quantize_fp4")
-    return _fp4_product(f, codes, scales, ss, x_ts, w, w_scales, w_ts, offsets, out, T, N, K, E, status)
+    wss = w_scales.shape[-1]
+    if T <= 32 * E:       # few rows: aligned rows of scales
+        w_scales, wss = _aligned_scales(w_scales, f)
+    nbytes = _fp4_workspace_bytes(True, f, T, N, K, E)
+    space = w.new_empty(nbytes)
+    p = _Fp4Product(f, T, N, K, E, _VALUE_DTYPES[out.dtype], x.data_ptr(), None, 0, x_ts, w.data_ptr(),
+                    w_scales.data_ptr(), wss, w_ts, _addr(offsets), out.data_ptr(), space.data_ptr(), nbytes,
+                    _addr(status))
+    _check(lib().moe_fp4_linear(p, code, rs, _current(x)), "moe_fp4_linear")
+    return out
 
 
 class MoELayer:

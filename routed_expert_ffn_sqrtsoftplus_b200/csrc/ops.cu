@@ -56,6 +56,65 @@ bool product_shape_ok(int32_t T, int32_t N, int32_t K, int32_t E) {
 }
 // Products whose tiles hold at most 32 tokens (fp4_plan): no workspace.
 bool few_rows(int32_t T, int32_t E) { return T <= 32ll * E; }
+// Alignment of their scale rows.
+int scale_unit(int32_t format) { return format == MOE_FP4_NV ? 16 : 8; }
+// Bytes of a row of quantised scales in moe_fp4_linear's workspace.
+int64_t padded_scales(int32_t format, int32_t K) { return (K / (format == MOE_FP4_NV ? 16 : 32) + 15) / 16 * 16; }
+
+// What moe_fp4_matmul and moe_fp4_linear check alike.
+moe_status check_product(const moe_fp4_product& p) {
+  if (!fp4_format_ok(p.format) || p.T < 0 || p.N < 1 || p.K < 1 || p.E < 1 || p.K % 32 != 0 ||
+      value_bytes(p.out_dtype) == 0)
+    return MOE_ERR_INVALID_ARG;
+  if (p.offsets == nullptr && p.E != 1) return MOE_ERR_INVALID_ARG;
+  if (p.w_scale_stride < p.K / (p.format == MOE_FP4_NV ? 16 : 32)) return MOE_ERR_INVALID_ARG;
+  if (p.format == MOE_FP4_MX && (p.x_tensor_scale != nullptr || p.w_tensor_scale != nullptr))
+    return MOE_ERR_INVALID_ARG;
+  if (!product_shape_ok(p.T, p.N, p.K, p.E)) return MOE_ERR_UNSUPPORTED;
+  if (p.T == 0) return MOE_OK;
+  if (p.w == nullptr || p.w_scales == nullptr || p.y == nullptr) return MOE_ERR_INVALID_ARG;
+  if (!aligned(p.w, 16) || !aligned(p.y, value_bytes(p.out_dtype)) || !aligned(p.offsets, 4) ||
+      !aligned(p.x_tensor_scale, 4) || !aligned(p.w_tensor_scale, 4) || !aligned(p.status, 4) ||
+      !aligned(p.workspace, 16))
+    return MOE_ERR_INVALID_ARG;
+  const int unit = scale_unit(p.format);
+  if (few_rows(p.T, p.E) && (p.w_scale_stride % unit != 0 || !aligned(p.w_scales, unit))) return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
+// The launches of a checked product.
+moe_status run_product(const moe_fp4_product& p, cudaStream_t stream) {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return launched(cudaErrorInvalidDevice);
+  Fp4GemmArgs a{};
+  a.xs = p.x_scales;
+  a.ws = p.w_scales;
+  a.xs_stride = p.x_scale_stride;
+  a.ws_stride = p.w_scale_stride;
+  a.sf_cols = p.K / (p.format == MOE_FP4_NV ? 16 : 32);
+  a.x_ts = p.x_tensor_scale;
+  a.w_ts = p.w_tensor_scale;
+  a.offsets = p.offsets;
+  a.T = p.T;
+  a.N = p.N;
+  a.E = p.E;
+  a.num_kb = (p.K + 255) / 256;
+  a.out = p.y;
+  a.out_dtype = p.out_dtype;
+  a.status = p.status;
+  a.timeout_ns = kWaitNs;
+  const Fp4Plan plan = fp4_plan(p.T, p.N, p.E, a.num_kb, sms);
+  if (p.workspace_bytes < fp4_workspace(p.format, p.T, p.N, p.E, a.num_kb, plan)) return MOE_ERR_INVALID_ARG;
+  a.splits = plan.splits;
+  a.m_tiles = (p.N + plan.cols - 1) / plan.cols;
+  CUtensorMap tw, tx;
+  if (!encode_tmap_bytes(&tw, p.w, static_cast<uint64_t>(p.E) * p.N, p.K / 2, plan.cols) ||
+      !encode_tmap_bytes(&tx, p.x, p.T, p.K / 2, 32))
+    return MOE_ERR_CUDA;
+  return launched(launch_gemm_fp4(p.format, tw, tx, a, p.workspace, plan, sms, stream));
+}
 
 }  // namespace
 
@@ -178,63 +237,53 @@ int64_t moe_fp4_workspace_bytes(int32_t format, int32_t T, int32_t N, int32_t K,
 }
 
 moe_status moe_fp4_matmul(const moe_fp4_product* p, moe_stream_t stream) {
-  if (p == nullptr || !fp4_format_ok(p->format)) return MOE_ERR_INVALID_ARG;
-  if (p->T < 0 || p->N < 1 || p->K < 1 || p->E < 1 || p->K % 32 != 0 || value_bytes(p->out_dtype) == 0)
-    return MOE_ERR_INVALID_ARG;
-  if (p->offsets == nullptr && p->E != 1) return MOE_ERR_INVALID_ARG;
+  if (p == nullptr) return MOE_ERR_INVALID_ARG;
+  moe_status st = check_product(*p);
+  if (st != MOE_OK || p->T == 0) return st;
+  if (p->x == nullptr || p->x_scales == nullptr || !aligned(p->x, 16)) return MOE_ERR_INVALID_ARG;
   const int cols = p->K / (p->format == MOE_FP4_NV ? 16 : 32);
-  if (p->x_scale_stride < cols || p->w_scale_stride < cols) return MOE_ERR_INVALID_ARG;
-  if (p->format == MOE_FP4_MX && (p->x_tensor_scale != nullptr || p->w_tensor_scale != nullptr))
-    return MOE_ERR_INVALID_ARG;
-  if (!product_shape_ok(p->T, p->N, p->K, p->E)) return MOE_ERR_UNSUPPORTED;
-  if (p->T == 0) return MOE_OK;
-  if (p->x == nullptr || p->x_scales == nullptr || p->w == nullptr || p->w_scales == nullptr || p->y == nullptr)
-    return MOE_ERR_INVALID_ARG;
-  if (!aligned(p->x, 16) || !aligned(p->w, 16) || !aligned(p->y, value_bytes(p->out_dtype)) ||
-      !aligned(p->offsets, 4) || !aligned(p->x_tensor_scale, 4) || !aligned(p->w_tensor_scale, 4) ||
-      !aligned(p->status, 4) || !aligned(p->workspace, 16))
-    return MOE_ERR_INVALID_ARG;
+  if (p->x_scale_stride < cols) return MOE_ERR_INVALID_ARG;
   if (few_rows(p->T, p->E)) {
-    const int unit = p->format == MOE_FP4_NV ? 16 : 8;
-    if (p->x_scale_stride % unit != 0 || p->w_scale_stride % unit != 0 || !aligned(p->x_scales, unit) ||
-        !aligned(p->w_scales, unit))
-      return MOE_ERR_INVALID_ARG;
+    const int unit = scale_unit(p->format);
+    if (p->x_scale_stride % unit != 0 || !aligned(p->x_scales, unit)) return MOE_ERR_INVALID_ARG;
   } else if (p->workspace == nullptr) {
     return MOE_ERR_INVALID_ARG;
   }
-  const moe_status st = on_device({p->x, p->x_scales, p->w, p->w_scales, p->y, p->offsets, p->x_tensor_scale,
-                                   p->w_tensor_scale, p->status, p->workspace});
+  st = on_device({p->x, p->x_scales, p->w, p->w_scales, p->y, p->offsets, p->x_tensor_scale, p->w_tensor_scale,
+                  p->status, p->workspace});
   if (st != MOE_OK) return st;
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return launched(cudaErrorInvalidDevice);
-  Fp4GemmArgs a{};
-  a.xs = p->x_scales;
-  a.ws = p->w_scales;
-  a.xs_stride = p->x_scale_stride;
-  a.ws_stride = p->w_scale_stride;
-  a.sf_cols = cols;
-  a.x_ts = p->x_tensor_scale;
-  a.w_ts = p->w_tensor_scale;
-  a.offsets = p->offsets;
-  a.T = p->T;
-  a.N = p->N;
-  a.E = p->E;
-  a.num_kb = (p->K + 255) / 256;
-  a.out = p->y;
-  a.out_dtype = p->out_dtype;
-  a.status = p->status;
-  a.timeout_ns = kWaitNs;
-  const Fp4Plan plan = fp4_plan(p->T, p->N, p->E, a.num_kb, sms);
-  if (p->workspace_bytes < fp4_workspace(p->format, p->T, p->N, p->E, a.num_kb, plan)) return MOE_ERR_INVALID_ARG;
-  a.splits = plan.splits;
-  a.m_tiles = (p->N + plan.cols - 1) / plan.cols;
-  CUtensorMap tw, tx;
-  if (!encode_tmap_bytes(&tw, p->w, static_cast<uint64_t>(p->E) * p->N, p->K / 2, plan.cols) ||
-      !encode_tmap_bytes(&tx, p->x, p->T, p->K / 2, 32))
-    return MOE_ERR_CUDA;
-  return launched(launch_gemm_fp4(p->format, tw, tx, a, p->workspace, plan, sms, as_stream(stream)));
+  return run_product(*p, as_stream(stream));
+}
+
+int64_t moe_fp4_linear_workspace_bytes(int32_t format, int32_t T, int32_t N, int32_t K, int32_t E) {
+  if (!fp4_format_ok(format) || !product_shape_ok(T, N, K, E) || K % 32 != 0 || T == 0) return 0;
+  return T * (K / 2 + padded_scales(format, K)) + moe_fp4_workspace_bytes(format, T, N, K, E);
+}
+
+moe_status moe_fp4_linear(const moe_fp4_product* p, int32_t x_dtype, int64_t x_row_stride, moe_stream_t stream) {
+  if (p == nullptr) return MOE_ERR_INVALID_ARG;
+  moe_status st = check_product(*p);
+  if (st != MOE_OK || p->T == 0) return st;
+  const int vb = value_bytes(x_dtype);
+  if (vb == 0 || x_row_stride < p->K || p->x == nullptr || !aligned(p->x, vb) || p->workspace == nullptr)
+    return MOE_ERR_INVALID_ARG;
+  if (p->workspace_bytes < moe_fp4_linear_workspace_bytes(p->format, p->T, p->N, p->K, p->E)) return MOE_ERR_INVALID_ARG;
+  st = on_device({p->x, p->w, p->w_scales, p->y, p->offsets, p->x_tensor_scale, p->w_tensor_scale, p->status,
+                  p->workspace});
+  if (st != MOE_OK) return st;
+  // the workspace: codes, scales in rows padded to 16 bytes (read in whole vectors), the product's own
+  moe_fp4_product q = *p;
+  uint8_t* codes = static_cast<uint8_t*>(p->workspace);
+  q.x = codes;
+  q.x_scale_stride = padded_scales(p->format, p->K);
+  uint8_t* scales = codes + static_cast<int64_t>(p->T) * (p->K / 2);
+  q.x_scales = scales;
+  q.workspace = scales + p->T * q.x_scale_stride;
+  q.workspace_bytes = p->workspace_bytes - p->T * (p->K / 2 + q.x_scale_stride);
+  st = launched(launch_quantize_fp4(p->format, p->x, x_dtype, p->T, p->K, x_row_stride, p->x_tensor_scale, codes, scales,
+                                    q.x_scale_stride, as_stream(stream)));
+  if (st != MOE_OK) return st;
+  return run_product(q, as_stream(stream));
 }
 
 }  // extern "C"

@@ -97,10 +97,24 @@ def _product(**kw):
     (dict(T=33), INV), (dict(T=33, workspace=FAKE + 8), INV)])
 def test_fp4_matmul_refuses_bad_arguments(L, kw, want):
     assert L.moe_fp4_matmul(_product(**kw), None) == want
+    if not any(n.startswith("x_scale") for n in kw) and "workspace" not in kw and kw.get("format") != 1:
+        # the same with x to be quantised: x's scales are not given, and there is always a workspace
+        big = dict(dict(workspace=FAKE, workspace_bytes=1 << 40), **kw)
+        if kw.get("x", 0) != FAKE + 4 and kw.get("T") != 33:
+            assert L.moe_fp4_linear(_product(**big), 2, 1 << 20, None) == want
     assert L.moe_fp4_matmul(None, None) == INV
     w = L.moe_fp4_workspace_bytes
     assert w(0, 32, 64, 64, 1) == 0 and w(1, 33, 64, 64, 1) > 0 and w(0, 64, 64, 64, 2) == 0 and w(2, 99, 64, 64, 1) == 0
     assert w(0, -1, 64, 64, 1) == 0 and w(0, 99, 0, 64, 1) == 0 and w(0, 99, 64, 64, 513) == 0
+
+
+def test_fp4_linear_refuses_bad_arguments(L):
+    w = L.moe_fp4_linear_workspace_bytes
+    assert w(0, 4, 64, 64, 1) == 4 * (32 + 16) and w(0, 4, 64, 48, 1) == 0 and w(0, 0, 64, 64, 1) == 0
+    f = lambda dt=0, rs=64, **kw: L.moe_fp4_linear(_product(**dict(dict(workspace=FAKE, workspace_bytes=1 << 20), **kw)), dt, rs, None)  # noqa: E731
+    assert f(dt=3) == INV and f(rs=63) == INV and f(x=FAKE + 1) == INV and f(x=None) == INV
+    assert f(workspace=None) == INV and f(workspace_bytes=4 * 48 - 1) == INV and f(workspace=FAKE + 8) == INV
+    assert L.moe_fp4_linear(None, 0, 64, None) == INV and f(T=0) == OK
 
 
 def test_bindings_refuse_bad_tensors(L):
