@@ -532,17 +532,16 @@ MOE_API moe_status moe_dequantize_fp4(int32_t format, const uint8_t* codes, cons
  * in fp32 and rounded once to y's type.
  *   x [T, K/2], w [E, N, K/2] codes, 16-byte aligned; K % 32 == 0
  *   x_scales, w_scales: K/32 or K/16 bytes per row, rows *_scale_stride bytes apart; nothing
- *          behind a row's last scale is read. Up to 32 rows per expert (T <= 32 E), base and
+ *          behind a row's last scale is read. Where the call needs no workspace, base and
  *          stride are multiples of 8 (MXFP4) or 16 (NVFP4) bytes (moe_fp4_pad_scales makes such
- *          rows of others); beyond, any
+ *          rows of others); otherwise any
  *   x_tensor_scale fp32 [1], w_tensor_scale fp32 [E] (device) or NULL; NVFP4 only
  *   offsets int32 [E + 1] device: rows offsets[g] .. offsets[g + 1] meet w[g]. Rows in none of
  *          these ranges (behind the last, in front of the first) are left as they were. Values are
  *          clamped to [0, T] and to ascending order. NULL: E = 1, every row.
  *   y [T, N] contiguous, out_dtype (moe_value_dtype)
- *   workspace: moe_fp4_workspace_bytes(...) bytes, 16-byte aligned (NULL where that is 0, which it
- *          is for T <= 32 E); scratch of this call, free once the stream is through it. Two calls
- *          that may overlap need one each
+ *   workspace: moe_fp4_workspace_bytes(...) bytes, 16-byte aligned (NULL where that is 0); scratch
+ *          of this call, free once the stream is through it. Two calls that may overlap need one each
  *   status: int32 device word that a wait which ran out sets to 1, or NULL
  * Limits: T <= 2^22, N and K <= 2^18, E <= 512. No allocation, no synchronisation.
  */
@@ -570,7 +569,8 @@ typedef struct {
 MOE_API moe_status moe_fp4_pad_scales(const uint8_t* src, int64_t rows, int32_t cols, uint8_t* dst,
                                       int64_t dst_stride, moe_stream_t stream);
 
-/* Bytes of workspace of such a product (0 also for arguments that moe_fp4_matmul refuses). */
+/* Bytes of workspace of such a product on the current device (0 also for shapes that moe_fp4_matmul
+ * refuses). Few rows need none. */
 MOE_API int64_t moe_fp4_workspace_bytes(int32_t format, int32_t T, int32_t N, int32_t K, int32_t E);
 
 MOE_API moe_status moe_fp4_matmul(const moe_fp4_product* p, moe_stream_t stream);

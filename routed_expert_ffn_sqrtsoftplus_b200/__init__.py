@@ -408,7 +408,7 @@ def _fp4_out(x, T, N, out, out_dtype):
 
 
 def _aligned_scales(scales, f):
-    """(scales, row stride) with rows that a product of few rows can read: as they are, or padded copies."""
+    """(scales, row stride) with rows that a product without a workspace can read: as they are, or padded copies."""
     cols = scales.shape[-1]
     if (cols | scales.data_ptr()) % (16 if f else 8) == 0:
         return scales, cols
@@ -420,7 +420,7 @@ def _aligned_scales(scales, f):
 
 
 @functools.lru_cache(maxsize=4096)
-def _fp4_workspace_bytes(linear, *shape):
+def _fp4_workspace_bytes(linear, device, *shape):
     L = lib()
     return (L.moe_fp4_linear_workspace_bytes if linear else L.moe_fp4_workspace_bytes)(*shape)
 
@@ -460,10 +460,10 @@ def fp4_matmul(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_scale
     _same_device(x, x_scales=x_scales, w=w, w_scales=w_scales, x_tensor_scale=x_tensor_scale,
                  w_tensor_scale=w_tensor_scale, offsets=offsets, out=out, status=status)
     xss, wss = x_scales.shape[1], w_scales.shape[-1]
-    if T <= 32 * E:       # few rows: no workspace, but aligned rows of scales
+    nbytes = _fp4_workspace_bytes(False, x.device.index, f, T, N, K, E)
+    if nbytes == 0:       # the scales are read as they are: aligned rows
         w_scales, wss = _aligned_scales(w_scales, f)
         x_scales, xss = _aligned_scales(x_scales, f)
-    nbytes = _fp4_workspace_bytes(False, f, T, N, K, E)
     space = w.new_empty(nbytes)
     p = _Fp4Product(f, T, N, K, E, _VALUE_DTYPES[out.dtype], x.data_ptr(), x_scales.data_ptr(), xss, x_ts,
                     w.data_ptr(), w_scales.data_ptr(), wss, w_ts, _addr(offsets), out.data_ptr(),
@@ -497,9 +497,9 @@ def fp4_linear(x: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor, fmt: st
     _same_device(x, w=w, w_scales=w_scales, x_tensor_scale=x_tensor_scale, w_tensor_scale=w_tensor_scale,
                  offsets=offsets, out=out, status=status)
     wss = w_scales.shape[-1]
-    if T <= 32 * E:       # few rows: aligned rows of scales
+    if _fp4_workspace_bytes(False, x.device.index, f, T, N, K, E) == 0:   # the scales are read as they are
         w_scales, wss = _aligned_scales(w_scales, f)
-    nbytes = _fp4_workspace_bytes(True, f, T, N, K, E)
+    nbytes = _fp4_workspace_bytes(True, x.device.index, f, T, N, K, E)
     space = w.new_empty(nbytes)
     p = _Fp4Product(f, T, N, K, E, _VALUE_DTYPES[out.dtype], x.data_ptr(), None, 0, x_ts, w.data_ptr(),
                     w_scales.data_ptr(), wss, w_ts, _addr(offsets), out.data_ptr(), space.data_ptr(), nbytes,

@@ -177,6 +177,9 @@ __global__ void __launch_bounds__(256)
     quantize_fp4_kernel(const T* __restrict__ src, uint32_t runs, FastDiv per_row, int64_t row_stride, int vec,
                         const float* __restrict__ tensor_scale, uint2* __restrict__ codes,
                         uint8_t* __restrict__ scales, int64_t scale_stride) {
+  // A product's prologue, which then waits for these codes. Not beside a grid of many rounds, whose blocks
+  // would find the SMs taken by those that wait.
+  if (gridDim.x <= 128) let_next_kernel_start();
   const uint32_t first = blockIdx.x * (256u * kRuns<T, kNv>) + threadIdx.x;
   Raw<T> raw[kRuns<T, kNv>];
 #pragma unroll

@@ -73,7 +73,9 @@ struct Cfg {
   static constexpr int kBlocks = kHalves + kBBlocks;
   static constexpr int kBlockBytes = 128 * kRowSf;
   static constexpr int kRawBytes = kBlocks * kBlockBytes;
-  static constexpr int kASfBytes = kHalves * kAtoms * 512, kBSfBytes = kBBlocks * kAtoms * 512;  // = kRawBytes
+  // bytes of a stage's arranged scales of w and of x: kRawBytes together
+  [[maybe_unused]] static constexpr int kASfBytes = kHalves * kAtoms * 512;
+  [[maybe_unused]] static constexpr int kBSfBytes = kBBlocks * kAtoms * 512;
   static constexpr int kFixed = 1024 + 512 + 2 * (kMaxExperts + 1) * 4;  // alignment, barriers, experts
   // stages of scales in flight: as the tiles' where they come together, else six
   static constexpr int kFit = kPre ? (227 * 1024 - kFixed) / (kABytes + kBBytes + kRawBytes)
@@ -151,29 +153,30 @@ __device__ __forceinline__ void st_cluster_f32(uint32_t saddr, uint32_t rank, fl
       : "memory");
 }
 
-// mbarrier.try_wait that may suspend the thread for up to kSuspendNs (it wakes when the phase
-// completes). With the default limit the dozen waiting warps poll shared memory hard enough to
-// slow the MMAs' own reads of it.
-constexpr uint32_t kSuspendNs = 1000000;
-__device__ __forceinline__ bool try_wait_suspend(uint64_t* bar, uint32_t parity) {
+// mbarrier.try_wait that may suspend the thread for up to 20 us (it wakes when the phase completes).
+__device__ __forceinline__ bool try_wait_suspended(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 20000;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}\n"
       : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity), "r"(kSuspendNs)
+      : "r"(smem_u32(bar)), "r"(parity)
       : "memory");
   return ok != 0;
 }
-
 // The slow path of a wait, kept out of line: the roles' loops have to stay small (their warps share
 // the SM's instruction caches).
 __device__ __noinline__ bool wait_longer(uint64_t* bar, uint32_t parity, unsigned long long timeout_ns, int* status,
                                          volatile int* abort_flag) {
   const uint64_t t0 = globaltimer_ns();
+  // a short wait polls (a suspended thread wakes some 300 ns late); a long one, a whole tile's say,
+  // stays out of the way of the MMAs' reads of shared memory
+#pragma unroll 1
+  for (int i = 0; i < 64; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
   while (true) {
-    if (try_wait_suspend(bar, parity)) return true;
+    if (try_wait_suspended(bar, parity)) return true;
     if (*abort_flag) return false;
     if (globaltimer_ns() - t0 > timeout_ns) {
       *abort_flag = 1;
@@ -184,14 +187,19 @@ __device__ __noinline__ bool wait_longer(uint64_t* bar, uint32_t parity, unsigne
 }
 __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, const Fp4GemmArgs& a,
                                               volatile int* abort_flag) {
-  return try_wait_suspend(bar, parity) || wait_longer(bar, parity, a.timeout_ns, a.status, abort_flag);
+  return mbar_try_wait(bar, parity) || wait_longer(bar, parity, a.timeout_ns, a.status, abort_flag);
 }
-// The same by a whole converged warp, which leaves it together: the loop branches on a vote alone and
-// calls nothing, so that the code around it keeps its addresses in uniform registers. Bounded by the
-// number of tries, each of which returns after kSuspendNs at the latest.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint32_t tries) {
-  for (uint32_t i = 0; !__all_sync(0xffffffffu, try_wait_suspend(bar, parity)); ++i)
-    if (i >= tries) return false;
+// The same by a whole converged warp, which leaves it together: the loop branches on votes alone and
+// calls nothing, so that the code around it keeps its addresses in uniform registers.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, unsigned long long timeout_ns) {
+  uint64_t t0 = 0;
+  for (uint32_t i = 0; !__all_sync(0xffffffffu, mbar_try_wait(bar, parity)); ++i) {
+    if ((i & 255u) == 255u) {
+      const uint64_t now = globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      if (__any_sync(0xffffffffu, now - t0 > timeout_ns)) return false;
+    }
+  }
   return true;
 }
 
@@ -412,6 +420,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(tmem_base_smem, 512);
     tmem_relinquish();
   }
+  // everything above overlaps the kernel in front (the quantiser, or the scales' arrangement)
+  wait_for_previous_kernel();
   if (warp == kFirstSf) scan_experts<C::kTokens>(args.offsets, args.E, args.T, pre, row_s);
   tc_fence_before();
   __syncthreads();
@@ -490,7 +500,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     // once the stage before this one is through.
     const bool elected = elect_one();
     const uint32_t tmem = uniform(tmem_base);
-    const uint32_t tries = static_cast<uint32_t>(args.timeout_ns / kSuspendNs);
     const uint64_t tile_desc = sdesc_sw128(smem_u32(sA)), raw_desc = sdesc_plain(smem_u32(sRaw));
     const uint32_t a_lo0 = static_cast<uint32_t>(tile_desc), hi = static_cast<uint32_t>(tile_desc >> 32);
     const uint32_t b_lo0 = static_cast<uint32_t>(sdesc_sw128(smem_u32(sB)));
@@ -515,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     bool ok = true;
     if (kPre && t0 < total) {
-      ok = warp_wait(&full[0], 0, tries);
+      ok = warp_wait(&full[0], 0, args.timeout_ns);
       tc_fence_after();
       if (elected) copy_scales(0, 0, 0, C::kBlocks);
       __syncwarp();
@@ -528,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++n_stage;
         return true;
       }
-      const bool w = warp_wait(&slot[old], ophase, tries);
+      const bool w = warp_wait(&slot[old], ophase, args.timeout_ns);
       if (++old == C::kRaw) {
         old = 0;
         ophase ^= 1;
@@ -539,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Tile tl = tile_of<C>(t, args, pre, row_s);
       const uint32_t n_mma = (tl.rows + 15) & ~15;
       const uint32_t idesc = uniform(idesc_fp4(kNv, n_mma));
-      ok = warp_wait(&tempty[acc], aphase ^ 1, tries);
+      ok = warp_wait(&tempty[acc], aphase ^ 1, args.timeout_ns);
       if (!ok) break;
       tc_fence_after();
       const uint32_t d = tmem + acc * C::kAccCols;
@@ -568,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t nphase = stage + 1 == C::kStages ? phase ^ 1 : phase;
           const int nset = set + 1 == C::kSets ? 0 : set + 1;
           if (kb + 1 < kb1 || t + stride < total) {
-            ok = warp_wait(&full[nstage], nphase, tries) && set_free();
+            ok = warp_wait(&full[nstage], nphase, args.timeout_ns) && set_free();
             if (!ok) break;
             tc_fence_after();
           }
@@ -585,8 +594,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           phase = nphase;
           set = nset;
         } else {
-          ok = warp_wait(&rturned[raw], rphase, tries) && (kb == kb0 && t == t0 ? true : set_free()) &&
-               warp_wait(&full[stage], phase, tries);
+          ok = warp_wait(&rturned[raw], rphase, args.timeout_ns) && (kb == kb0 && t == t0 ? true : set_free()) &&
+               warp_wait(&full[stage], phase, args.timeout_ns);
           if (!ok) break;
           tc_fence_after();
           if (elected) {
@@ -845,12 +854,14 @@ cudaError_t launch_cfg(const CUtensorMap& tw, const CUtensorMap& tx, const Fp4Ge
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = C::kSmemBytes;
   cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = kSplit ? a.splits : 1;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = kSplit ? a.splits : 1;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = kSplit ? 1 : 0;
+  cfg.numAttrs = kSplit ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, tw, tx, a);
 }
 
@@ -893,6 +904,7 @@ template <bool kNv, int kTokens, int kCols>
 __global__ void __launch_bounds__(256) arrange_scales_kernel(const Fp4GemmArgs a) {
   constexpr int kWords = kNv ? 4 : 2;
   __shared__ int pre[kMaxExperts + 1], row_s[kMaxExperts + 1];
+  wait_for_previous_kernel();
   if (threadIdx.x < 32) scan_experts<kTokens>(a.offsets, a.E, a.T, pre, row_s);
   __syncthreads();
   int tile = blockIdx.x;
@@ -923,8 +935,16 @@ __global__ void __launch_bounds__(256) arrange_scales_kernel(const Fp4GemmArgs a
 template <bool kNv, int kTokens, int kCols>
 cudaError_t launch_arrange(const Fp4GemmArgs& a, int64_t xtiles, cudaStream_t s) {
   const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(a.E) * a.m_tiles + xtiles), (a.num_kb + 3) / 4);
-  arrange_scales_kernel<kNv, kTokens, kCols><<<grid, 256, 0, s>>>(a);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, arrange_scales_kernel<kNv, kTokens, kCols>, a);
 }
 
 template <bool kNv>
@@ -933,13 +953,17 @@ cudaError_t launch_fmt(const CUtensorMap& tw, const CUtensorMap& tx, const Fp4Ge
   const int64_t xtiles = a.E == 1 ? (a.T + p.tokens - 1) / p.tokens : a.T / p.tokens + (a.E < a.T ? a.E : a.T);
   const int64_t most = xtiles * a.m_tiles;
   if (p.tokens > 32) {
-    const cudaError_t e = p.tokens == 96 ? launch_arrange<kNv, 96, 256>(a, xtiles, s) : launch_arrange<kNv, 192, 256>(a, xtiles, s);
+    const cudaError_t e = p.tokens == 192 ? launch_arrange<kNv, 192, 256>(a, xtiles, s)
+                          : p.cols == 256 ? launch_arrange<kNv, 96, 256>(a, xtiles, s)
+                                          : launch_arrange<kNv, 96, 128>(a, xtiles, s);
     if (e != cudaSuccess) return e;
   }
   if (p.splits > 1) return launch_cfg<kNv, false, 1, 32, true>(tw, tx, a, static_cast<int>(most) * p.splits, s);
   const int grid = static_cast<int>(most < num_sms ? most : num_sms);
-  if (p.cols == 128) return launch_cfg<kNv, false, 1, 32, false>(tw, tx, a, grid, s);
-  if (p.tokens == 32) return launch_cfg<kNv, false, 2, 32, false>(tw, tx, a, grid, s);
+  if (p.tokens == 32)
+    return p.cols == 128 ? launch_cfg<kNv, false, 1, 32, false>(tw, tx, a, grid, s)
+                         : launch_cfg<kNv, false, 2, 32, false>(tw, tx, a, grid, s);
+  if (p.cols == 128) return launch_cfg<kNv, true, 1, 96, false>(tw, tx, a, grid, s);
   if (p.tokens == 96) return launch_cfg<kNv, true, 2, 96, false>(tw, tx, a, grid, s);
   return launch_cfg<kNv, true, 2, 192, false>(tw, tx, a, grid, s);
 }
@@ -959,9 +983,6 @@ int64_t fp4_workspace(int format, int T, int N, int E, int num_kb, const Fp4Plan
   return num_kb * (wt * tile_sf_bytes(format, p.cols) + token_tiles(T, E, p.tokens) * tile_sf_bytes(format, p.tokens));
 }
 
-// Tile shape. Up to 32 rows per expert (on average, where there are several) a tile is 32 tokens
-// wide; its height is 256 rows of w where that still gives every SM a tile, else 128, and
-// where even those leave SMs idle a cluster shares each tile's K.
 static int max_clusters(int size) {
   // per device and size, asked once: what a device can hold does not change
   constexpr int kDevices = 64;
@@ -992,24 +1013,49 @@ static int max_clusters(int size) {
   return n;
 }
 
-Fp4Plan fp4_plan(int T, int N, int E, int num_kb, int num_sms) {
-  Fp4Plan p{32, 256, 1};
-  const int per = (T + E - 1) / E;
-  if (per > 32) {
-    p.tokens = per > 96 ? 192 : 96;
-    return p;
-  }
-  const int experts = E < T ? E : T;
-  if (static_cast<int64_t>(experts) * ((N + 255) / 256) >= num_sms) return p;
-  p.cols = 128;
-  const int tiles = experts * ((N + 127) / 128);
-  // a cluster's CTAs sit in one GPC, whose SMs are no multiple of every size: a second round of
-  // clusters costs more than it brings (36 tiles, 4 CTAs each: 33 clusters fit, 14.7 us; 3 each XXX)
+// Largest number of CTAs per cluster with which `tiles` clusters are on the device at once and each has a K
+// block. A cluster's CTAs sit in one GPC, whose SMs are no multiple of every size: a second round of clusters
+// costs more than it brings (36 tiles: 14.7 us with 4 CTAs each, of which 33 clusters fit, 8.2 us with 3).
+static int splits_for(int64_t tiles, int num_kb) {
   for (int s = kMaxSplits; s > 1; --s)
-    if (s <= num_kb && tiles <= max_clusters(s)) {
-      p.splits = s;
-      break;
+    if (s <= num_kb && tiles <= max_clusters(s)) return s;
+  return 1;
+}
+
+// Tile shape. Up to 32 rows per expert (on average, where there are several) a tile is 32 tokens wide; its
+// height is 256 rows of w where that still gives every SM a tile, else 128, and where even those leave SMs
+// idle a cluster shares each tile's K. With more rows, the shape whose rounds of tiles cost least; several
+// experts' weights, which HBM bounds, are read in wide token tiles only.
+Fp4Plan fp4_plan(int T, int N, int E, int num_kb, int num_sms) {
+  // ns of each shape: once (launches, the arrangement of the scales, the first stages), per tile (epilogue),
+  // per stage; fitted to eleven shapes from 48 x 4608 x 5120 to 4096 x 1024 x 1024, which they meet to 15 %
+  constexpr struct {
+    int tokens, cols, once, tile, stage;
+  } kShapes[] = {{192, 256, 6000, 5000, 560},
+                 {96, 256, 6000, 2700, 455},
+                 {96, 128, 6000, 2500, 325},
+                 {32, 256, 4700, 300, 530},
+                 {32, 128, 4100, 1600, 290}};
+  constexpr int kJoin = 1300;  // a split tile's sum
+  const int per = (T + E - 1) / E, experts = E < T ? E : T;
+  Fp4Plan p{32, 256, 1};
+  int64_t least = INT64_MAX;
+  for (const auto& sh : kShapes) {
+    if (per <= 32 ? sh.tokens > 32 : E > 1 && sh.tokens == 32) continue;
+    // one matrix: its tiles; several: an expert's last tile is half full on average
+    const int64_t tok = E == 1      ? (T + sh.tokens - 1) / sh.tokens
+                        : per <= 32 ? experts
+                                    : T / sh.tokens + (E + 1) / 2;
+    const int64_t tiles = tok * ((N + sh.cols - 1) / sh.cols);
+    int splits = 1;
+    if (sh.tokens == 32 && sh.cols == 128) splits = splits_for(tiles, num_kb);
+    const int64_t rounds = (tiles + num_sms - 1) / num_sms, stages = (num_kb + splits - 1) / splits;
+    const int64_t cost = sh.once + rounds * (sh.tile + stages * sh.stage) + (splits > 1 ? kJoin : 0);
+    if (cost < least) {
+      least = cost;
+      p = Fp4Plan{sh.tokens, sh.cols, splits};
     }
+  }
   return p;
 }
 

@@ -54,9 +54,7 @@ bool fp4_format_ok(int32_t f) { return f == MOE_FP4_MX || f == MOE_FP4_NV; }
 bool product_shape_ok(int32_t T, int32_t N, int32_t K, int32_t E) {
   return T >= 0 && N >= 1 && K >= 1 && E >= 1 && T <= 1 << 22 && N <= 1 << 18 && K <= 1 << 18 && E <= 512;
 }
-// Products whose tiles hold at most 32 tokens (fp4_plan): no workspace.
-bool few_rows(int32_t T, int32_t E) { return T <= 32ll * E; }
-// Alignment of their scale rows.
+// Alignment of scale rows that are read as they are (by a product without a workspace).
 int scale_unit(int32_t format) { return format == MOE_FP4_NV ? 16 : 8; }
 // Bytes of a row of quantised scales in moe_fp4_linear's workspace.
 int64_t padded_scales(int32_t format, int32_t K) { return (K / (format == MOE_FP4_NV ? 16 : 32) + 15) / 16 * 16; }
@@ -77,13 +75,33 @@ moe_status check_product(const moe_fp4_product& p) {
       !aligned(p.x_tensor_scale, 4) || !aligned(p.w_tensor_scale, 4) || !aligned(p.status, 4) ||
       !aligned(p.workspace, 16))
     return MOE_ERR_INVALID_ARG;
-  const int unit = scale_unit(p.format);
-  if (few_rows(p.T, p.E) && (p.w_scale_stride % unit != 0 || !aligned(p.w_scales, unit))) return MOE_ERR_INVALID_ARG;
   return MOE_OK;
 }
 
+// The shape of its tiles, and its workspace.
+struct Planned {
+  Fp4Plan plan;
+  int64_t bytes;
+};
+Planned plan_product(int32_t format, int32_t T, int32_t N, int32_t K, int32_t E) {
+  const int num_kb = (K + 255) / 256;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    cudaGetLastError();
+  if (sms < 1) sms = 148;  // no device: what a B200 would need
+  const Fp4Plan plan = fp4_plan(T, N, E, num_kb, sms);
+  return Planned{plan, fp4_workspace(format, T, N, E, num_kb, plan)};
+}
+// Where the scales are read as they are, their rows are aligned.
+bool scales_ok(const moe_fp4_product& p, const Planned& planned) {
+  const int unit = scale_unit(p.format);
+  return planned.bytes > 0 || (p.w_scale_stride % unit == 0 && aligned(p.w_scales, unit) &&
+                               p.x_scale_stride % unit == 0 && aligned(p.x_scales, unit));
+}
+
 // The launches of a checked product.
-moe_status run_product(const moe_fp4_product& p, cudaStream_t stream) {
+moe_status run_product(const moe_fp4_product& p, const Fp4Plan& plan, cudaStream_t stream) {
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
@@ -105,8 +123,6 @@ moe_status run_product(const moe_fp4_product& p, cudaStream_t stream) {
   a.out_dtype = p.out_dtype;
   a.status = p.status;
   a.timeout_ns = kWaitNs;
-  const Fp4Plan plan = fp4_plan(p.T, p.N, p.E, a.num_kb, sms);
-  if (p.workspace_bytes < fp4_workspace(p.format, p.T, p.N, p.E, a.num_kb, plan)) return MOE_ERR_INVALID_ARG;
   a.splits = plan.splits;
   a.m_tiles = (p.N + plan.cols - 1) / plan.cols;
   CUtensorMap tw, tx;
@@ -227,13 +243,7 @@ moe_status moe_fp4_pad_scales(const uint8_t* src, int64_t rows, int32_t cols, ui
 
 int64_t moe_fp4_workspace_bytes(int32_t format, int32_t T, int32_t N, int32_t K, int32_t E) {
   if (!fp4_format_ok(format) || !product_shape_ok(T, N, K, E) || T == 0) return 0;
-  const int num_kb = (K + 255) / 256;
-  int dev = 0, sms = 0;
-  // without a device the shape alone decides, as on any
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    cudaGetLastError();
-  return fp4_workspace(format, T, N, E, num_kb, fp4_plan(T, N, E, num_kb, sms));
+  return plan_product(format, T, N, K, E).bytes;
 }
 
 moe_status moe_fp4_matmul(const moe_fp4_product* p, moe_stream_t stream) {
@@ -243,16 +253,13 @@ moe_status moe_fp4_matmul(const moe_fp4_product* p, moe_stream_t stream) {
   if (p->x == nullptr || p->x_scales == nullptr || !aligned(p->x, 16)) return MOE_ERR_INVALID_ARG;
   const int cols = p->K / (p->format == MOE_FP4_NV ? 16 : 32);
   if (p->x_scale_stride < cols) return MOE_ERR_INVALID_ARG;
-  if (few_rows(p->T, p->E)) {
-    const int unit = scale_unit(p->format);
-    if (p->x_scale_stride % unit != 0 || !aligned(p->x_scales, unit)) return MOE_ERR_INVALID_ARG;
-  } else if (p->workspace == nullptr) {
+  const Planned planned = plan_product(p->format, p->T, p->N, p->K, p->E);
+  if (!scales_ok(*p, planned) || p->workspace_bytes < planned.bytes || (planned.bytes > 0 && p->workspace == nullptr))
     return MOE_ERR_INVALID_ARG;
-  }
   st = on_device({p->x, p->x_scales, p->w, p->w_scales, p->y, p->offsets, p->x_tensor_scale, p->w_tensor_scale,
                   p->status, p->workspace});
   if (st != MOE_OK) return st;
-  return run_product(*p, as_stream(stream));
+  return run_product(*p, planned.plan, as_stream(stream));
 }
 
 int64_t moe_fp4_linear_workspace_bytes(int32_t format, int32_t T, int32_t N, int32_t K, int32_t E) {
@@ -267,23 +274,26 @@ moe_status moe_fp4_linear(const moe_fp4_product* p, int32_t x_dtype, int64_t x_r
   const int vb = value_bytes(x_dtype);
   if (vb == 0 || x_row_stride < p->K || p->x == nullptr || !aligned(p->x, vb) || p->workspace == nullptr)
     return MOE_ERR_INVALID_ARG;
-  if (p->workspace_bytes < moe_fp4_linear_workspace_bytes(p->format, p->T, p->N, p->K, p->E)) return MOE_ERR_INVALID_ARG;
-  st = on_device({p->x, p->w, p->w_scales, p->y, p->offsets, p->x_tensor_scale, p->w_tensor_scale, p->status,
-                  p->workspace});
-  if (st != MOE_OK) return st;
+  const Planned planned = plan_product(p->format, p->T, p->N, p->K, p->E);
+  const int64_t xs_stride = padded_scales(p->format, p->K), own = p->T * (p->K / 2 + xs_stride);
+  if (p->workspace_bytes < own + planned.bytes) return MOE_ERR_INVALID_ARG;
   // the workspace: codes, scales in rows padded to 16 bytes (read in whole vectors), the product's own
   moe_fp4_product q = *p;
   uint8_t* codes = static_cast<uint8_t*>(p->workspace);
   q.x = codes;
-  q.x_scale_stride = padded_scales(p->format, p->K);
+  q.x_scale_stride = xs_stride;
   uint8_t* scales = codes + static_cast<int64_t>(p->T) * (p->K / 2);
   q.x_scales = scales;
-  q.workspace = scales + p->T * q.x_scale_stride;
-  q.workspace_bytes = p->workspace_bytes - p->T * (p->K / 2 + q.x_scale_stride);
+  q.workspace = codes + own;
+  q.workspace_bytes = p->workspace_bytes - own;
+  if (!scales_ok(q, planned)) return MOE_ERR_INVALID_ARG;
+  st = on_device({p->x, p->w, p->w_scales, p->y, p->offsets, p->x_tensor_scale, p->w_tensor_scale, p->status,
+                  p->workspace});
+  if (st != MOE_OK) return st;
   st = launched(launch_quantize_fp4(p->format, p->x, x_dtype, p->T, p->K, x_row_stride, p->x_tensor_scale, codes, scales,
                                     q.x_scale_stride, as_stream(stream)));
   if (st != MOE_OK) return st;
-  return run_product(q, as_stream(stream));
+  return run_product(q, planned.plan, as_stream(stream));
 }
 
 }  // extern "C"

@@ -94,18 +94,20 @@ def _product(**kw):
     (dict(x=FAKE + 4), INV), (dict(y=FAKE + 1), INV), (dict(y=None), INV), (dict(w_scales=None), INV),
     (dict(offsets=FAKE + 2), INV), (dict(T=(1 << 22) + 1), UNS), (dict(E=513, offsets=FAKE), UNS),
     (dict(N=(1 << 18) + 1), UNS), (dict(T=0, x=None, y=None), OK),
-    (dict(T=33), INV), (dict(T=33, workspace=FAKE + 8), INV)])
+    (dict(T=4096, N=4096, K=4096, x_scale_stride=128, w_scale_stride=128), INV),
+    (dict(T=4096, N=4096, K=4096, x_scale_stride=128, w_scale_stride=128, workspace=FAKE, workspace_bytes=999), INV),
+    (dict(T=4096, workspace=FAKE + 8, workspace_bytes=1 << 40), INV)])
 def test_fp4_matmul_refuses_bad_arguments(L, kw, want):
     assert L.moe_fp4_matmul(_product(**kw), None) == want
     if not any(n.startswith("x_scale") for n in kw) and "workspace" not in kw and kw.get("format") != 1:
         # the same with x to be quantised: x's scales are not given, and there is always a workspace
         big = dict(dict(workspace=FAKE, workspace_bytes=1 << 40), **kw)
-        if kw.get("x", 0) != FAKE + 4 and kw.get("T") != 33:
+        if kw.get("x", 0) != FAKE + 4 and kw.get("T") != 4096:
             assert L.moe_fp4_linear(_product(**big), 2, 1 << 20, None) == want
     assert L.moe_fp4_matmul(None, None) == INV
     w = L.moe_fp4_workspace_bytes
-    assert w(0, 32, 64, 64, 1) == 0 and w(1, 33, 64, 64, 1) > 0 and w(0, 64, 64, 64, 2) == 0 and w(2, 99, 64, 64, 1) == 0
-    assert w(0, -1, 64, 64, 1) == 0 and w(0, 99, 0, 64, 1) == 0 and w(0, 99, 64, 64, 513) == 0
+    assert w(0, 32, 64, 64, 1) == 0 and w(1, 4096, 4096, 4096, 1) > 0 and w(0, 64, 64, 64, 2) == 0 and w(2, 4096, 4096, 4096, 1) == 0
+    assert w(0, -1, 64, 64, 1) == 0 and w(0, 4096, 0, 4096, 1) == 0 and w(0, 99, 64, 64, 513) == 0
 
 
 def test_fp4_linear_refuses_bad_arguments(L):
