@@ -539,7 +539,7 @@ MOE_API moe_status moe_dequantize_fp4(int32_t format, const uint8_t* codes, cons
  *   offsets int32 [E + 1] device: rows offsets[g] .. offsets[g + 1] meet w[g]. Rows in none of
  *          these ranges (behind the last, in front of the first) are left as they were. Values are
  *          clamped to [0, T] and to ascending order. NULL: E = 1, every row.
- *   y [T, N] contiguous, out_dtype (moe_value_dtype)
+ *   y [T, N] contiguous, out_dtype (moe_value_dtype), may not be x
  *   workspace: moe_fp4_workspace_bytes(...) bytes, 16-byte aligned (NULL where that is 0); scratch
  *          of this call, free once the stream is through it. Two calls that may overlap need one each
  *   status: int32 device word that a wait which ran out sets to 1, or NULL

@@ -416,12 +416,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tmA);
     tma_prefetch_desc(&tmB);
   }
+  // everything above overlaps the kernel in front (the quantiser, or the scales' arrangement); TMEM is taken
+  // behind it, so that no block waits for a kernel that waits for this block's columns
+  wait_for_previous_kernel();
   if (warp == 1) {
     tmem_alloc(tmem_base_smem, 512);
     tmem_relinquish();
   }
-  // everything above overlaps the kernel in front (the quantiser, or the scales' arrangement)
-  wait_for_previous_kernel();
   if (warp == kFirstSf) scan_experts<C::kTokens>(args.offsets, args.E, args.T, pre, row_s);
   tc_fence_before();
   __syncthreads();
@@ -576,12 +577,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int nstage = stage + 1 == C::kStages ? 0 : stage + 1;
           const uint32_t nphase = stage + 1 == C::kStages ? phase ^ 1 : phase;
           const int nset = set + 1 == C::kSets ? 0 : set + 1;
-          if (kb + 1 < kb1 || t + stride < total) {
-            ok = warp_wait(&full[nstage], nphase, args.timeout_ns) && set_free();
-            if (!ok) break;
-            tc_fence_after();
-          }
-          // no branch in here: behind the last stage of all, the copies bring what nothing reads
+          if (kb + 1 < kb1 || t + stride < total) ok = warp_wait(&full[nstage], nphase, args.timeout_ns);
+          ok = ok && set_free();
+          if (!ok) break;
+          tc_fence_after();
+          // no branch in here: behind the last stage of all, the copies bring what nothing reads, to
+          // columns that nothing reads any more
           // (with the copies under a condition the compiler gave up the uniform registers of the whole
           // region, and a stage took 1510 cycles instead of 920)
           if (elected) {

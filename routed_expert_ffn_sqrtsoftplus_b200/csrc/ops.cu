@@ -250,7 +250,7 @@ moe_status moe_fp4_matmul(const moe_fp4_product* p, moe_stream_t stream) {
   if (p == nullptr) return MOE_ERR_INVALID_ARG;
   moe_status st = check_product(*p);
   if (st != MOE_OK || p->T == 0) return st;
-  if (p->x == nullptr || p->x_scales == nullptr || !aligned(p->x, 16)) return MOE_ERR_INVALID_ARG;
+  if (p->x == nullptr || p->x_scales == nullptr || !aligned(p->x, 16) || p->x == p->y) return MOE_ERR_INVALID_ARG;
   const int cols = p->K / (p->format == MOE_FP4_NV ? 16 : 32);
   if (p->x_scale_stride < cols) return MOE_ERR_INVALID_ARG;
   const Planned planned = plan_product(p->format, p->T, p->N, p->K, p->E);
@@ -272,7 +272,8 @@ moe_status moe_fp4_linear(const moe_fp4_product* p, int32_t x_dtype, int64_t x_r
   moe_status st = check_product(*p);
   if (st != MOE_OK || p->T == 0) return st;
   const int vb = value_bytes(x_dtype);
-  if (vb == 0 || x_row_stride < p->K || p->x == nullptr || !aligned(p->x, vb) || p->workspace == nullptr)
+  if (vb == 0 || x_row_stride < p->K || p->x == nullptr || !aligned(p->x, vb) || p->x == p->y ||
+      p->workspace == nullptr)
     return MOE_ERR_INVALID_ARG;
   const Planned planned = plan_product(p->format, p->T, p->N, p->K, p->E);
   const int64_t xs_stride = padded_scales(p->format, p->K), own = p->T * (p->K / 2 + xs_stride);

@@ -265,6 +265,100 @@ def test_strided_x_streams_and_graphs():
         assert torch.equal(yg, moe.fp4_linear(x[:T, :384], w[0], ws[0], "nvfp4", x_tensor_scale=ts, w_tensor_scale=wts))
 
 
+def test_many_calls_at_once_on_several_streams():
+    """Calls on streams that are not ordered with each other, of every tile shape, beside one another."""
+    shapes = [(1, 640, 2304), (40, 1024, 1024), (130, 512, 512), (600, 2304, 768), (9, 5120, 2304)]
+    cases = []
+    for i, (T, N, K) in enumerate(shapes):
+        x = torch.randn((T, K), generator=_gen(i)).to(torch.bfloat16).cuda()
+        w, ws, _ = _weights(1, N, K, FMT[i % 2], i)
+        cases.append((x, w[0], ws[0], FMT[i % 2]))
+    want = [moe.fp4_linear(*c) for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in shapes]
+    got = [[moe.fp4_linear(*c, stream=s) for c, s in zip(cases, streams)] for _ in range(10)]
+    torch.cuda.synchronize()
+    for row in got:
+        assert all(torch.equal(a, b) for a, b in zip(row, want))
+
+
+def test_first_call_of_a_process_may_be_captured():
+    import subprocess
+    import sys
+    code = """
+import torch, routed_expert_ffn_sqrtsoftplus_b200 as moe
+x = torch.randn(40, 512, device='cuda').to(torch.bfloat16)
+big = torch.randn(900, 512, device='cuda').to(torch.bfloat16)
+w = torch.randint(0, 256, (384, 256), dtype=torch.uint8, device='cuda')
+s = torch.randint(118, 124, (384, 16), dtype=torch.uint8, device='cuda')
+z = torch.randn(70, 64, device='cuda')
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    outs = [moe.fp4_linear(x[:1], w, s, 'mxfp4'), moe.fp4_linear(x, w, s, 'mxfp4'), moe.fp4_linear(big, w, s, 'mxfp4')]
+    i, v = moe.route(z, 4, score='sigmoid', bias=z[0].contiguous(), n_groups=4, topk_groups=2)
+    d = moe.route_backward(v, z, i, score='sigmoid')
+g.replay(); torch.cuda.synchronize()
+again = [moe.fp4_linear(x[:1], w, s, 'mxfp4'), moe.fp4_linear(x, w, s, 'mxfp4'), moe.fp4_linear(big, w, s, 'mxfp4')]
+assert all(torch.equal(a, b) for a, b in zip(outs, again))
+j, u = moe.route(z, 4, score='sigmoid', bias=z[0].contiguous(), n_groups=4, topk_groups=2)
+assert torch.equal(i, j) and torch.equal(u, v) and torch.equal(d, moe.route_backward(u, z, j, score='sigmoid'))
+print('captured')
+"""
+    import os
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert "captured" in r.stdout, r.stderr[-2000:]
+
+
+def test_two_graphs_of_one_call_do_not_share_their_workspace():
+    xs = [torch.randn((300, 512), generator=_gen(i)).to(torch.bfloat16).cuda() for i in range(2)]
+    w, ws, _ = _weights(1, 512, 512, "nvfp4", 7)
+    graphs, outs = [], []
+    for x in xs:
+        moe.fp4_linear(x, w[0], ws[0], "nvfp4")
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(moe.fp4_linear(x, w[0], ws[0], "nvfp4"))
+        graphs.append(g)
+    want = [moe.fp4_linear(x, w[0], ws[0], "nvfp4") for x in xs]
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
+def test_offsets_beyond_32_bits():
+    """More than 2^31 elements in x (quantisation) and in y (the product): the last rows are right."""
+    rows, K = 70000, 32768
+    x = torch.zeros((rows, K), dtype=torch.bfloat16, device="cuda")
+    tail = torch.randn((2, K), generator=_gen(1)).to(torch.bfloat16)
+    x[-2:] = tail.cuda()
+    codes, scales = moe.quantize_fp4(x, "mxfp4")
+    rc, rs, rv = ref.quantize(tail.double().numpy(), "mxfp4")
+    assert np.array_equal(codes[-2:].cpu().numpy(), rc) and np.array_equal(scales[-2:].cpu().numpy(), rs)
+    assert int(codes[:-2].max()) == 0
+    del x
+    v = moe.dequantize_fp4(codes, scales, "mxfp4")
+    assert np.array_equal(v[-2:].double().cpu().numpy(), rv)
+    del v, codes, scales
+    T, N, K = 1100000, 2048, 32
+    x = torch.zeros((T, K), dtype=torch.bfloat16, device="cuda")
+    tail = torch.randn((3, K), generator=_gen(2)).to(torch.bfloat16)
+    x[-3:] = tail.cuda()
+    w, ws, _ = _weights(1, N, K, "mxfp4", 3)
+    y = moe.fp4_linear(x, w[0], ws[0], "mxfp4")
+    _, _, xv = ref.quantize(tail.double().numpy(), "mxfp4")
+    wv = ref.values(w[0].cpu().numpy(), ws[0].cpu().numpy(), "mxfp4")
+    want = xv @ wv.T
+    assert (np.abs(y[-3:].double().cpu().numpy() - want) <= _bound(xv, wv, want, torch.bfloat16)).all()
+    assert float(y[:-3].abs().max()) == 0.0
+
+
 def test_route_then_experts():
     """A 4-bit expert layer from the operators: route, sort by expert, gate and up, SwiGLU, down, weighted sum."""
     T, E, H, I, k = 37, 8, 256, 128, 2

@@ -81,7 +81,7 @@ def test_fp4_refuses_bad_arguments(L):
 
 def _product(**kw):
     d = dict(format=0, T=4, N=64, K=64, E=1, out_dtype=0, x=FAKE, x_scales=FAKE, x_scale_stride=8, x_tensor_scale=None,
-             w=FAKE, w_scales=FAKE, w_scale_stride=8, w_tensor_scale=None, offsets=None, y=FAKE, workspace=None, workspace_bytes=0, status=None)
+             w=FAKE, w_scales=FAKE, w_scale_stride=8, w_tensor_scale=None, offsets=None, y=FAKE + 64, workspace=None, workspace_bytes=0, status=None)
     d.update(kw)
     return moe._Fp4Product(*[d[n] for n, _ in moe._Fp4Product._fields_])
 
@@ -91,7 +91,7 @@ def _product(**kw):
     (dict(E=2), INV), (dict(out_dtype=3), INV), (dict(x_scale_stride=1), INV), (dict(format=1), INV), (dict(w_scale_stride=12), INV),
     (dict(K=512), INV), (dict(x_scales=FAKE + 4), INV), (dict(format=1, x_scale_stride=16, w_scale_stride=16, w_scales=FAKE + 8), INV),
     (dict(x_tensor_scale=FAKE), INV), (dict(w_tensor_scale=FAKE), INV), (dict(x=None), INV), (dict(w=FAKE + 8), INV),
-    (dict(x=FAKE + 4), INV), (dict(y=FAKE + 1), INV), (dict(y=None), INV), (dict(w_scales=None), INV),
+    (dict(x=FAKE + 4), INV), (dict(y=FAKE + 1), INV), (dict(y=FAKE), INV), (dict(y=None), INV), (dict(w_scales=None), INV),
     (dict(offsets=FAKE + 2), INV), (dict(T=(1 << 22) + 1), UNS), (dict(E=513, offsets=FAKE), UNS),
     (dict(N=(1 << 18) + 1), UNS), (dict(T=0, x=None, y=None), OK),
     (dict(T=4096, N=4096, K=4096, x_scale_stride=128, w_scale_stride=128), INV),
