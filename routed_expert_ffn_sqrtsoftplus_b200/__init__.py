@@ -231,9 +231,10 @@ def _current(t: torch.Tensor) -> int:
 
 
 def _same_device(ref: torch.Tensor, **tensors):
+    dev = ref.device
     for n, t in tensors.items():
-        if t is not None and t.device != ref.device:
-            raise ValueError(f"{n} is on {t.device}, expected {ref.device}")
+        if t is not None and t.device != dev:
+            raise ValueError(f"{n} is on {t.device}, expected {dev}")
 
 
 def _rows(t: torch.Tensor, name: str):
@@ -245,15 +246,17 @@ def _rows(t: torch.Tensor, name: str):
         raise ValueError(f"{name} must be bfloat16, float16 or float32, got {t.dtype}")
     if t.dim() != 2:
         raise ValueError(f"{name} must have 2 dimensions, got {t.dim()}")
-    r, c = t.shape
-    if c > 1 and t.stride(1) != 1:
+    (r, c), (rs, cs) = t.shape, t.stride()
+    if c > 1 and cs != 1:
         raise ValueError(f"{name} must have contiguous rows")
-    rs = t.stride(0) if r > 1 else c
-    if rs < c:
+    if r <= 1:
+        rs = c
+    elif rs < c:
         raise ValueError(f"{name} must not have overlapping rows")
     return r, c, rs, code
 
 
+@functools.lru_cache(maxsize=1024)
 def _route_config(E, k, n_groups, topk_groups, score, group_score, renormalize, route_scale):
     if score not in SCORES:
         raise ValueError(f"score must be one of {tuple(SCORES)}")

@@ -593,8 +593,10 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
 //                 sqrtsoftplus  dz_j = scale p_j (g_j - gbar) sigmoid(z_j) / (2 softplus(z_j))
 //   otherwise:    sigmoid, sqrtsoftplus: s_j in the place of p_j and gbar = 0
 //                 softmax       dz_e = s_e (scale g_e [e selected] - scale sum_j g_j s_j), every e
-// One warp per row; lane r holds slot r. The row is written once, 16 bytes a lane, each
-// vector gathering the slots that fall into it (an expert named twice adds up).
+// One warp per row; lane r holds slot r (an expert named twice adds up). Where only the selected
+// experts have gradients the row is written as zeros, 16 bytes a lane, and the slots go over them;
+// the dense form reads the row twice (the second time from the caches) and writes it once, each
+// vector gathering the slots that fall into it.
 template <typename T>
 __global__ void __launch_bounds__(kRouteWarps * 32)
     route_grad_kernel(const float* __restrict__ grad_w, const T* __restrict__ logits, int64_t row_stride,
@@ -660,35 +662,58 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
     d = has ? scale * p * (g - gbar) * slope : 0.f;
   }
   T* orow = out + static_cast<size_t>(t) * E;
+  // an expert named twice: its first slot takes the sum
+  const uint32_t same = __match_any_sync(kFull, e);
+  bool lead = has && __ffs(same) - 1 == lane;
+  if (__any_sync(kFull, has && (same & (same - 1)) != 0u)) {
+    float sum = 0.f;
+    for (int r = 0; r < k; ++r) {
+      const float dr = __shfl_sync(kFull, d, r);
+      if ((same >> r) & 1u) sum += dr;
+    }
+    d = sum;
+  }
+  if (!dense) {
+    // zeros, 16 bytes a lane, then the slots' elements over them (one warp: in this order)
+    for (int c = lane * V; c < E; c += 32 * V) {
+      if (vec_out && c + V <= E) {
+        *reinterpret_cast<uint4*>(orow + c) = make_uint4(0u, 0u, 0u, 0u);
+      } else {
+        for (int i = 0; i < V && c + i < E; ++i) orow[c + i] = from_f32<T>(0.f);
+      }
+    }
+    __syncwarp();
+    if (lead) orow[e] = from_f32<T>(d);
+    return;
+  }
   for (int c0 = 0; c0 < E; c0 += 32 * V) {
     const int c = c0 + lane * V;
     float acc[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[i] = 0.f;
-    for (int r = 0; r < k; ++r) {
+    for (uint32_t left = __ballot_sync(kFull, lead); left != 0u; left &= left - 1u) {
+      const int r = __ffs(left) - 1;
       const int er = __shfl_sync(kFull, e, r);
       const float dr = __shfl_sync(kFull, d, r);
-      if (er >= 0) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) acc[i] += er == c + i ? dr : 0.f;
-      }
+      for (int i = 0; i < V; ++i) acc[i] = er == c + i ? dr : acc[i];
     }
-    if (dense && c < E) {
+    if (c < E) {
       float z[V];
       load_run<T, V>(row + c, min(V, E - c), vec_in != 0, z);
 #pragma unroll
       for (int i = 0; i < V; ++i) acc[i] = z[i] == -INFINITY ? 0.f : expf(z[i] - zmax) * inv_sum * (acc[i] - back);
-    }
-    if (vec_out && c + V <= E) {
-      uint4 o;
-      T* ot = reinterpret_cast<T*>(&o);
+      if (vec_out && c + V <= E) {
+        uint4 o;
+        T* ot = reinterpret_cast<T*>(&o);
 #pragma unroll
-      for (int i = 0; i < V; ++i) ot[i] = from_f32<T>(acc[i]);
-      *reinterpret_cast<uint4*>(orow + c) = o;
-    } else {
+        for (int i = 0; i < V; ++i) ot[i] = from_f32<T>(acc[i]);
+        *reinterpret_cast<uint4*>(orow + c) = o;
+      } else {
 #pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (c + i < E) orow[c + i] = from_f32<T>(acc[i]);
+        for (int i = 0; i < V; ++i)
+          if (c + i < E) orow[c + i] = from_f32<T>(acc[i]);
+      }
     }
   }
 }
