@@ -164,6 +164,7 @@ struct SelectArgs {
   int E, G, kept, k, score, sum2;
   int Eg;          // experts of a group
   int lane_shift;  // a group is 2^lane_shift whole lanes, or -1
+  int scan_shift;  // else 2^scan_shift lanes scan it (G groups: at most 32 lanes)
 };
 
 // Maximum and sum of a softmax row in 64 bits.
@@ -341,15 +342,19 @@ __device__ __forceinline__ int select_by_rounds(uint32_t (&key)[EPL], int e0, in
 
 // By a list: the k-th largest of the lanes' maxima bounds the k-th largest key from below, and few keys
 // reach that bound. They go to a list of at most 32 (key, expert), one a lane, and each counts those ahead of
-// it. -1 where there are more (many equal keys); `tol` lowers the bound, so that the list also holds what
+// it. -1 where there are more; `tol` lowers the bound, so that the list also holds what
 // floats cannot tell from the last slot. Some 200 instructions where rounds take 60 each.
-constexpr int kListK = 12;  // above, the bound lets too many through
+constexpr int kListK = 16;  // above, the bound lets too many through (half the lanes: 22 on average)
 template <int EPL>
 __device__ __forceinline__ int select_by_list(const uint32_t (&key)[EPL], int e0, int k, float tol, uint2* list,
                                               int lane, int& mine, uint32_t& mkey) {
   uint32_t bk = 0u;
 #pragma unroll
   for (int i = 0; i < EPL; ++i) bk = max(bk, key[i]);
+  // the k-th maximum of few more than k lanes (the others' groups are out) is a low one: the list would
+  // overflow (of 4 k / 3 lanes with 16 keys each some 21 reach it, of k lanes all)
+  const int live = __popc(__ballot_sync(kFull, bk != 0u));
+  if (4 * k > 3 * live && live * EPL > 32) return -1;
   uint32_t bound = 0u;
   int reached = 0;
   for (int r = 0; r < k && reached < k; ++r) {  // equal maxima go together
@@ -458,36 +463,39 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
     // a group is a power of two of whole lanes: 2^lane_shift of them
     const bool whole = a.lane_shift >= 0;
     float w1 = -INFINITY, w2 = -INFINITY;
+    // the two largest of 2^shift lanes each, then lane g takes group g's
+    auto merge = [&](int shift) {
+      for (int o = 1; o < 1 << shift; o <<= 1) {
+        const float o1 = __shfl_xor_sync(kFull, w1, o), o2 = __shfl_xor_sync(kFull, w2, o);
+        w2 = fmaxf(fmaxf(w2, o2), fminf(w1, o1));
+        w1 = fmaxf(w1, o1);
+      }
+      const int src = min(lane, a.G - 1) << shift;
+      w1 = __shfl_sync(kFull, w1, src);
+      w2 = __shfl_sync(kFull, w2, src);
+    };
     if (whole) {
-      // merge the lanes' two largest
 #pragma unroll
       for (int i = 0; i < EPL; ++i) {
         w2 = fmaxf(w2, fminf(w1, v[i]));
         w1 = fmaxf(w1, v[i]);
       }
-      for (int o = 1; o < 1 << a.lane_shift; o <<= 1) {
-        const float o1 = __shfl_xor_sync(kFull, w1, o), o2 = __shfl_xor_sync(kFull, w2, o);
-        w2 = fmaxf(fmaxf(w2, o2), fminf(w1, o1));
-        w1 = fmaxf(w1, o1);
-      }
-      const int src = min(lane, a.G - 1) << a.lane_shift;  // lane g takes group g's
-      w1 = __shfl_sync(kFull, w1, src);
-      w2 = __shfl_sync(kFull, w2, src);
+      merge(a.lane_shift);
     } else {
       float* fb = reinterpret_cast<float*>(key_buf) + static_cast<size_t>(warp) * a.E;
 #pragma unroll
       for (int i = 0; i < EPL; ++i)
         if (e0 + i < a.E) fb[e0 + i] = v[i];
       __syncwarp();
-      if (lane < a.G) {
-        int j = lane % Eg;  // lanes start apart, so that a power-of-two group size does not hit one bank
-        for (int n = 0; n < Eg; ++n) {
-          const float x = fb[lane * Eg + j];
+      // 2^scan_shift lanes scan a group
+      const int g = lane >> a.scan_shift, step = 1 << a.scan_shift;
+      if (g < a.G)
+        for (int j = lane & (step - 1); j < Eg; j += step) {
+          const float x = fb[g * Eg + j];
           w2 = fmaxf(w2, fminf(w1, x));
           w1 = fmaxf(w1, x);
-          j = j + 1 == Eg ? 0 : j + 1;
         }
-      }
+      merge(a.scan_shift);
       __syncwarp();
     }
     float worth = a.sum2 && w2 != -INFINITY ? w1 + w2 : w1;
@@ -593,11 +601,10 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
 //                 sqrtsoftplus  dz_j = scale p_j (g_j - gbar) sigmoid(z_j) / (2 softplus(z_j))
 //   otherwise:    sigmoid, sqrtsoftplus: s_j in the place of p_j and gbar = 0
 //                 softmax       dz_e = s_e (scale g_e [e selected] - scale sum_j g_j s_j), every e
-// One warp per row; lane r holds slot r (an expert named twice adds up). Where only the selected
-// experts have gradients the row is written as zeros, 16 bytes a lane, and the slots go over them;
-// the dense form reads the row twice (the second time from the caches) and writes it once, each
-// vector gathering the slots that fall into it.
-template <typename T>
+// One warp per row; lane r holds slot r (an expert named twice adds up). The row is written 16 bytes a
+// lane without the slots' own terms (zeros, or in the dense form -s_e scale sum_j g_j s_j from a row held
+// in registers), and the slots' elements go over it: one warp, so in this order. Bound by HBM's writes.
+template <typename T, bool kDense>
 __global__ void __launch_bounds__(kRouteWarps * 32)
     route_grad_kernel(const float* __restrict__ grad_w, const T* __restrict__ logits, int64_t row_stride,
                       const int32_t* __restrict__ idx, int rows, int E, int k, int score, int renorm, float scale,
@@ -612,32 +619,67 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
   const bool has = e >= 0;
   const float g = has ? __ldg(grad_w + static_cast<size_t>(t) * k + lane) : 0.f;
   const float zs = has ? to_f32<T>(row[e]) : -INFINITY;
-  const bool dense = score == kScoreSoftmax && !renorm;
-  float zmax = -INFINITY, inv_sum = 0.f, back = 0.f;
-  float d = 0.f;  // the slot's own term
-  if (dense) {
-    float s = 0.f;
-    for (int c = lane * V; c < E; c += 32 * V) {
-      float z[V];
-      load_run<T, V>(row + c, min(V, E - c), vec_in != 0, z);
-      // running maximum and sum: one pass over the row
-      float m = zmax;
-#pragma unroll
-      for (int i = 0; i < V; ++i) m = fmaxf(m, z[i]);
-      if (m != -INFINITY) {
-        s *= expf(zmax - m);
-#pragma unroll
-        for (int i = 0; i < V; ++i) s += expf(z[i] - m);
-        zmax = m;
-      }
+  float d = 0.f;  // the slot's gradient
+  T* orow = out + static_cast<size_t>(t) * E;
+  // an expert named twice: its first slot takes the sum
+  const uint32_t same = __match_any_sync(kFull, e);
+  const bool lead = has && __ffs(same) - 1 == lane;
+  const bool twice = __any_sync(kFull, has && (same & (same - 1)) != 0u);
+  auto join = [&]() {
+    float sum = 0.f;
+    for (int r = 0; r < k; ++r) {
+      const float dr = __shfl_sync(kFull, d, r);
+      if ((same >> r) & 1u) sum += dr;
     }
-    const float m = warp_max(zmax);
-    s = m == -INFINITY ? 0.f : warp_sum(s * expf(zmax - m));
-    zmax = m;
-    inv_sum = s > 0.f || s != s ? __fdiv_rn(1.0f, s) : 0.f;
+    d = sum;
+  };
+  if constexpr (kDense) {
+    // the row in registers: its exponentials are taken once
+    constexpr int kChunks = 512 / (32 * V);
+    float z[kChunks][V];
+    float zmax = -INFINITY, s = 0.f;
+#pragma unroll
+    for (int u = 0; u < kChunks; ++u) {
+      const int c = (u * 32 + lane) * V;
+      load_run<T, V>(row + c, min(V, E - c), vec_in != 0, z[u]);
+#pragma unroll
+      for (int i = 0; i < V; ++i) zmax = fmaxf(zmax, z[u][i]);
+    }
+    zmax = warp_max(zmax);
+#pragma unroll
+    for (int u = 0; u < kChunks; ++u)
+      if (u * 32 * V < E) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          z[u][i] = z[u][i] == -INFINITY ? 0.f : expf(z[u][i] - zmax);  // an expert that is off, and a row of them: 0
+          s += z[u][i];
+        }
+      }
+    s = warp_sum(s);
+    const float inv_sum = s > 0.f || s != s ? __fdiv_rn(1.0f, s) : 0.f;
     const float sj = has && zs != -INFINITY ? expf(zs - zmax) * inv_sum : 0.f;
     d = scale * g;
-    back = warp_sum(d * sj);
+    const float back = warp_sum(d * sj);
+#pragma unroll
+    for (int u = 0; u < kChunks; ++u) {
+      const int c = (u * 32 + lane) * V;
+      if (c >= E) break;
+#pragma unroll
+      for (int i = 0; i < V; ++i) z[u][i] = -(z[u][i] * inv_sum) * back;
+      if (vec_out && c + V <= E) {
+        uint4 o;
+        T* ot = reinterpret_cast<T*>(&o);
+#pragma unroll
+        for (int i = 0; i < V; ++i) ot[i] = from_f32<T>(z[u][i]);
+        *reinterpret_cast<uint4*>(orow + c) = o;
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (c + i < E) orow[c + i] = from_f32<T>(z[u][i]);
+      }
+    }
+    if (twice) join();
+    d = sj * (d - back);
   } else {
     float p, gbar = 0.f;
     if (renorm) {
@@ -660,21 +702,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
       slope *= 0.5f;
     }
     d = has ? scale * p * (g - gbar) * slope : 0.f;
-  }
-  T* orow = out + static_cast<size_t>(t) * E;
-  // an expert named twice: its first slot takes the sum
-  const uint32_t same = __match_any_sync(kFull, e);
-  bool lead = has && __ffs(same) - 1 == lane;
-  if (__any_sync(kFull, has && (same & (same - 1)) != 0u)) {
-    float sum = 0.f;
-    for (int r = 0; r < k; ++r) {
-      const float dr = __shfl_sync(kFull, d, r);
-      if ((same >> r) & 1u) sum += dr;
-    }
-    d = sum;
-  }
-  if (!dense) {
-    // zeros, 16 bytes a lane, then the slots' elements over them (one warp: in this order)
+    if (twice) join();
     for (int c = lane * V; c < E; c += 32 * V) {
       if (vec_out && c + V <= E) {
         *reinterpret_cast<uint4*>(orow + c) = make_uint4(0u, 0u, 0u, 0u);
@@ -682,40 +710,9 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
         for (int i = 0; i < V && c + i < E; ++i) orow[c + i] = from_f32<T>(0.f);
       }
     }
-    __syncwarp();
-    if (lead) orow[e] = from_f32<T>(d);
-    return;
   }
-  for (int c0 = 0; c0 < E; c0 += 32 * V) {
-    const int c = c0 + lane * V;
-    float acc[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) acc[i] = 0.f;
-    for (uint32_t left = __ballot_sync(kFull, lead); left != 0u; left &= left - 1u) {
-      const int r = __ffs(left) - 1;
-      const int er = __shfl_sync(kFull, e, r);
-      const float dr = __shfl_sync(kFull, d, r);
-#pragma unroll
-      for (int i = 0; i < V; ++i) acc[i] = er == c + i ? dr : acc[i];
-    }
-    if (c < E) {
-      float z[V];
-      load_run<T, V>(row + c, min(V, E - c), vec_in != 0, z);
-#pragma unroll
-      for (int i = 0; i < V; ++i) acc[i] = z[i] == -INFINITY ? 0.f : expf(z[i] - zmax) * inv_sum * (acc[i] - back);
-      if (vec_out && c + V <= E) {
-        uint4 o;
-        T* ot = reinterpret_cast<T*>(&o);
-#pragma unroll
-        for (int i = 0; i < V; ++i) ot[i] = from_f32<T>(acc[i]);
-        *reinterpret_cast<uint4*>(orow + c) = o;
-      } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-          if (c + i < E) orow[c + i] = from_f32<T>(acc[i]);
-      }
-    }
-  }
+  __syncwarp();
+  if (lead) orow[e] = from_f32<T>(d);
 }
 
 template <typename T, int EPL>
@@ -731,7 +728,9 @@ cudaError_t launch_route_epl(const RouteArgs& r, cudaStream_t s) {
   int shift = -1;
   if (Eg % EPL == 0 && (lanes & (lanes - 1)) == 0)
     for (shift = 0; 1 << shift < lanes;) ++shift;
-  const SelectArgs a{r.E, r.n_groups, r.topk_groups, r.k, r.score, r.group_sum2, Eg, shift};
+  int scan = 0;
+  while (r.n_groups << (scan + 1) <= 32) ++scan;
+  const SelectArgs a{r.E, r.n_groups, r.topk_groups, r.k, r.score, r.group_sum2, Eg, shift, scan};
   route_kernel<T, EPL><<<(r.T + kRouteWarps - 1) / kRouteWarps, kRouteWarps * 32, smem, s>>>(
       static_cast<const T*>(r.logits), r.row_stride, r.bias, r.T, a, r.renorm, r.scale, vec ? 1 : 0,
       reinterpret_cast<uintptr_t>(r.bias) % 16 == 0 ? 1 : 0, r.idx, r.w);
@@ -750,7 +749,9 @@ template <typename T>
 cudaError_t launch_route_grad_t(const RouteGradArgs& r, cudaStream_t s) {
   const bool vi = reinterpret_cast<uintptr_t>(r.logits) % 16 == 0 && (r.row_stride * sizeof(T)) % 16 == 0;
   const bool vo = reinterpret_cast<uintptr_t>(r.out) % 16 == 0 && (r.E * sizeof(T)) % 16 == 0;
-  route_grad_kernel<T><<<(r.T + kRouteWarps - 1) / kRouteWarps, kRouteWarps * 32, 0, s>>>(
+  const bool dense = r.score == kScoreSoftmax && !r.renorm;
+  auto* kernel = dense ? route_grad_kernel<T, true> : route_grad_kernel<T, false>;
+  kernel<<<(r.T + kRouteWarps - 1) / kRouteWarps, kRouteWarps * 32, 0, s>>>(
       r.grad_w, static_cast<const T*>(r.logits), r.row_stride, r.idx, r.T, r.E, r.k, r.score, r.renorm, r.scale,
       vi ? 1 : 0, vo ? 1 : 0, static_cast<T*>(r.out));
   return cudaGetLastError();
@@ -786,7 +787,7 @@ cudaError_t launch_route(const RouteArgs& r, cudaStream_t s) {
 
 cudaError_t launch_route_grad(const RouteGradArgs& r, cudaStream_t s) {
   if (r.T == 0) return cudaSuccess;
-  if (r.k > 32) return cudaErrorInvalidValue;
+  if (r.k > 32 || r.E > 512) return cudaErrorInvalidValue;
   if (r.dtype == kValFp32) return launch_route_grad_t<float>(r, s);
   if (r.dtype == kValBf16) return launch_route_grad_t<__nv_bfloat16>(r, s);
   return launch_route_grad_t<__half>(r, s);
