@@ -275,6 +275,10 @@ __device__ __noinline__ int select_row_f64(const T* row, const float* bias, Sele
       rank += o > worth || (o == worth && g < lane);
     }
     keep = __ballot_sync(kFull, lane < a.G && rank < a.kept);
+    if (bias == nullptr) {  // the logits are the keys, only the groups' worth is a sum of scores
+      for (int e = lane; e < a.E; e += 32) buf[e] = to_f32<T>(row[e]);
+      __syncwarp();
+    }
   }
   int mine = -1;
   for (int r = 0; r < a.k; ++r) {
@@ -302,12 +306,12 @@ __device__ __noinline__ int select_row_f64(const T* row, const float* bias, Sele
 }
 
 // The k largest of the warp's keys (0: none) in order, lower expert first on a tie: lane r gets the r-th
-// expert and key, lane k the largest key left (0 if there is none); how many there are is returned.
+// expert and key, `left` the largest key left (0 if there is none); how many there are is returned.
 //
 // In rounds: a warp maximum (redux.sync) finds the next, and its lane looks for its next one.
 template <int EPL>
 __device__ __forceinline__ int select_by_rounds(uint32_t (&key)[EPL], int e0, int k, int lane, int& mine,
-                                                uint32_t& mkey) {
+                                                uint32_t& mkey, uint32_t& left) {
   uint32_t bk = 0u;
   int bi = 0, n = 0;
 #pragma unroll
@@ -317,10 +321,11 @@ __device__ __forceinline__ int select_by_rounds(uint32_t (&key)[EPL], int e0, in
       bi = i;
     }
 #pragma unroll 1
-  for (; n <= k; ++n) {
+  for (;; ++n) {
     const uint32_t m = __reduce_max_sync(kFull, bk);
-    if (lane == n) mkey = m;
+    left = m;
     if (n == k || m == 0u) break;
+    if (lane == n) mkey = m;
     const int win = __ffs(__ballot_sync(kFull, bk == m)) - 1;
     const int e = __shfl_sync(kFull, e0 + bi, win);
     if (lane == n) mine = e;
@@ -347,7 +352,7 @@ __device__ __forceinline__ int select_by_rounds(uint32_t (&key)[EPL], int e0, in
 constexpr int kListK = 16;  // above, the bound lets too many through (half the lanes: 22 on average)
 template <int EPL>
 __device__ __forceinline__ int select_by_list(const uint32_t (&key)[EPL], int e0, int k, float tol, uint2* list,
-                                              int lane, int& mine, uint32_t& mkey) {
+                                              int lane, int& mine, uint32_t& mkey, uint32_t& left) {
   uint32_t bk = 0u;
 #pragma unroll
   for (int i = 0; i < EPL; ++i) bk = max(bk, key[i]);
@@ -390,11 +395,12 @@ __device__ __forceinline__ int select_by_list(const uint32_t (&key)[EPL], int e0
   __syncwarp();
   if (lane < n) list[rank] = my;
   __syncwarp();
-  if (lane < n && lane <= k) {
+  if (lane < min(n, k)) {
     const uint2 o = list[lane];
     mkey = o.x;
-    if (lane < k) mine = static_cast<int>(o.y);
+    mine = static_cast<int>(o.y);
   }
+  left = n > k ? list[k].x : 0u;
   return min(n, k);
 }
 
@@ -482,7 +488,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
       }
       merge(a.lane_shift);
     } else {
-      float* fb = reinterpret_cast<float*>(key_buf) + static_cast<size_t>(warp) * a.E;
+      float* fb = reinterpret_cast<float*>(key_buf + static_cast<size_t>(warp) * a.E);  // this warp's alone
 #pragma unroll
       for (int i = 0; i < EPL; ++i)
         if (e0 + i < a.E) fb[e0 + i] = v[i];
@@ -498,7 +504,11 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
       merge(a.scan_shift);
       __syncwarp();
     }
-    float worth = a.sum2 && w2 != -INFINITY ? w1 + w2 : w1;
+    // half of the sum of two keys (the sum of two of the type's lowest values would be -infinity), off by
+    // no more than err
+    const bool two = a.sum2 && w2 != -INFINITY;
+    float worth = a.sum2 ? 0.5f * w1 + 0.5f * (two ? w2 : 0.f) : w1;
+    const float err = 0.5f * tol * (1.0f + (two ? 0.5f * fabsf(w1) + 0.5f * fabsf(w2) : fabsf(w1)));
     if (lane >= a.G) worth = -INFINITY;
     int rank = 0;
 #pragma unroll 4
@@ -509,11 +519,10 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
     const bool in = lane < a.G && rank < a.kept;
     uint32_t keep = __ballot_sync(kFull, in);
     if (need_scores) {
-      // the least of the kept and the best of the others, which lie side by side in the order
-      const float least = value_of(__reduce_min_sync(kFull, in ? key_of(worth) : kFull));
-      const uint32_t best_key = __reduce_max_sync(kFull, in || worth == -INFINITY ? 0u : key_of(worth));
-      const float best = value_of(best_key);
-      if (best_key != 0u && least - best <= 2.0f * tol * (1.0f + fabsf(best))) {
+      // the least that a kept group may be worth, and the most that another may
+      const uint32_t least = __reduce_min_sync(kFull, in ? key_of(worth - err) : kFull);
+      const uint32_t most = __reduce_max_sync(kFull, in || worth == -INFINITY ? 0u : key_of(worth + err));
+      if (least <= most) {
         // of each group, what reaches its second (or its first) key
         const float low = a.sum2 && w2 != -INFINITY ? w2 : w1;
         const float from = lane < a.G ? low - tol * (1.0f + fabsf(low)) : INFINITY;
@@ -554,13 +563,16 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
   }
 
   int mine = -1, n = 0;  // slot `lane`'s expert; slots filled
-  uint32_t mkey = 0u;    // its key; slot k's is the best one left
-  if (a.k <= kListK) n = select_by_list<EPL>(key, e0, a.k, bias != nullptr ? tol : 0.f, list_buf[warp], lane, mine, mkey);
-  if (a.k > kListK || n < 0) n = select_by_rounds<EPL>(key, e0, a.k, lane, mine, mkey);
+  uint32_t mkey = 0u, left = 0u;  // its key, and the best one left
+  if (a.k <= kListK)
+    n = select_by_list<EPL>(key, e0, a.k, bias != nullptr ? tol : 0.f, list_buf[warp], lane, mine, mkey, left);
+  if (a.k > kListK || n < 0) n = select_by_rounds<EPL>(key, e0, a.k, lane, mine, mkey, left);
   if (bias != nullptr) {
     // neighbours that 32-bit keys do not tell apart: order what reaches down to the last slot's key again
-    const float mine_f = value_of(mkey), up = __shfl_up_sync(kFull, mine_f, 1);
-    const bool close = lane > 0 && lane <= n && mkey != 0u && up - mine_f <= tol * (1.0f + fabsf(up));
+    uint32_t next = __shfl_down_sync(kFull, mkey, 1);
+    if (lane == n - 1) next = left;
+    const float mine_f = value_of(mkey);
+    const bool close = lane < n && next != 0u && mine_f - value_of(next) <= tol * (1.0f + fabsf(mine_f));
     if (!unsure && __any_sync(kFull, close)) {
       const float last = __shfl_sync(kFull, mine_f, n - 1);
       const float least = last - tol * (1.0f + fabsf(last));
@@ -731,7 +743,7 @@ cudaError_t launch_route_epl(const RouteArgs& r, cudaStream_t s) {
   int scan = 0;
   while (r.n_groups << (scan + 1) <= 32) ++scan;
   const SelectArgs a{r.E, r.n_groups, r.topk_groups, r.k, r.score, r.group_sum2, Eg, shift, scan};
-  route_kernel<T, EPL><<<(r.T + kRouteWarps - 1) / kRouteWarps, kRouteWarps * 32, smem, s>>>(
+  route_kernel<T, EPL><<<(r.T - 1) / kRouteWarps + 1, kRouteWarps * 32, smem, s>>>(
       static_cast<const T*>(r.logits), r.row_stride, r.bias, r.T, a, r.renorm, r.scale, vec ? 1 : 0,
       reinterpret_cast<uintptr_t>(r.bias) % 16 == 0 ? 1 : 0, r.idx, r.w);
   return cudaGetLastError();
@@ -751,7 +763,7 @@ cudaError_t launch_route_grad_t(const RouteGradArgs& r, cudaStream_t s) {
   const bool vo = reinterpret_cast<uintptr_t>(r.out) % 16 == 0 && (r.E * sizeof(T)) % 16 == 0;
   const bool dense = r.score == kScoreSoftmax && !r.renorm;
   auto* kernel = dense ? route_grad_kernel<T, true> : route_grad_kernel<T, false>;
-  kernel<<<(r.T + kRouteWarps - 1) / kRouteWarps, kRouteWarps * 32, 0, s>>>(
+  kernel<<<(r.T - 1) / kRouteWarps + 1, kRouteWarps * 32, 0, s>>>(
       r.grad_w, static_cast<const T*>(r.logits), r.row_stride, r.idx, r.T, r.E, r.k, r.score, r.renorm, r.scale,
       vi ? 1 : 0, vo ? 1 : 0, static_cast<T*>(r.out));
   return cudaGetLastError();

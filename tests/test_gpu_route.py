@@ -79,6 +79,62 @@ def test_route_near_ties_are_decided_as_in_64_bits():
         _check(z.cuda(), 7, kind, bias, G, kept)
 
 
+@pytest.mark.parametrize("k", [1, 8, 16, 17, 31, 32])
+def test_route_near_tie_at_the_last_slot(k):
+    # keys 0.01 apart, but for the last taken and the first left out: those are equal up to the bias' rounding
+    E = 48
+    g = torch.Generator().manual_seed(k)
+    for _ in range(24):
+        z = torch.randn((1, E), generator=g)
+        want = 1.0 - 0.01 * torch.arange(E).double()
+        want[k] = want[k - 1]
+        order = torch.randperm(E, generator=g)
+        bias = torch.empty(E)
+        bias[order] = (want - torch.sigmoid(z[0, order].double())).float()
+        _check(z.cuda(), k, "sigmoid", bias.cuda())
+
+
+def test_route_groups_whose_two_keys_cancel():
+    # keys near +-1000: a worth of about 1, of terms that 32 bits round to 2^-14
+    g = torch.Generator().manual_seed(11)
+    for Eg in (2, 3, 8):
+        E = 8 * Eg
+        z = 0.3 + 2e-5 * torch.randn((40, E), generator=g)
+        bias = torch.full((E,), -2000.0)
+        bias[0::Eg], bias[1::Eg] = 1000.0, -1000.0
+        _check(z.cuda(), 3, "sigmoid", bias.cuda(), 8, 3)
+
+
+def test_route_bias_of_the_lowest_value():
+    # two lowest values add to -infinity in 32 bits, but their group is not an empty one
+    z = torch.randn((5, 24), generator=torch.Generator().manual_seed(12))
+    z[:, :8] = -float("inf")
+    bias = torch.zeros(24)
+    bias[8:16] = torch.finfo(torch.float32).min
+    for group in ("top2", "max"):
+        idx, _ = _check(z.cuda(), 10, "sigmoid", bias.cuda(), 3, 2, group)
+        assert bool((idx[:, 8:].cpu() == torch.tensor([8, 9], dtype=torch.int32)).all())
+
+
+@pytest.mark.parametrize("E,G", [(200, 8), (100, 4), (480, 5), (512, 8), (64, 2)])
+def test_route_rows_that_64_bit_keys_decide(E, G):
+    """Every row is full of near ties, next to rows that are not: groups of whole lanes and others."""
+    g = torch.Generator().manual_seed(E)
+    z = torch.randn((64, E), generator=g)
+    z[::2] = z[0]
+    bias = (0.5 - torch.sigmoid(z[0].double())).float().cuda()
+    for kind in ("sigmoid", "softmax"):
+        _check(z.cuda(), 8, kind, bias, G, G // 2)
+
+
+def test_route_saturated_scores_keep_the_order_of_their_logits():
+    # sigmoid is 1 in 64 bits too: every group is worth the same, the logits still decide inside
+    z = 40.0 + torch.randperm(64, generator=torch.Generator().manual_seed(13)).float()[None].repeat(3, 1) / 8
+    idx, w = moe.route(z.cuda(), 6, score="sigmoid", n_groups=8, topk_groups=4)
+    want = torch.argsort(z[0, :32], descending=True)[:6].int()
+    assert bool((idx.cpu() == want).all()) and float((w - 1 / 6).abs().max()) <= TOL_W
+
+
 def test_route_exact_ties_take_the_lower_expert():
     z = torch.zeros((4, 96), device="cuda")
     z[1, 50:] = 1.0
