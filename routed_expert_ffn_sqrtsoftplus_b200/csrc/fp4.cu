@@ -119,6 +119,13 @@ __device__ __forceinline__ float e4m3_value(int code) {
 
 // The E4M3 code nearest to amax / (6 ts), ties to even, at most 126 (448).
 __device__ __forceinline__ int e4m3_scale(float amax, float ts) {
+  // far out, both by one power of two, so that neither the reciprocal nor a difference leaves the normal range
+  // (where amax does, the code is 0 or 126 with or without it)
+  if (ts < 0x1p-60f || ts > 0x1p60f) {
+    const float by = ts < 1.0f ? 0x1p60f : 0x1p-60f;
+    ts *= by;
+    amax *= by;
+  }
   const float q = amax * __frcp_rn(6.0f * ts);  // off by a few units of 2^-24: the code is right, or a neighbour
   int c = static_cast<int>(__nv_cvt_float_to_fp8(q, __NV_SATFINITE, __NV_E4M3)) & 0x7F;
   c = min(c, 126);
@@ -151,15 +158,17 @@ __device__ __forceinline__ uint32_t to_e2m1x8(const float* v, float scale) {
 
 // Decides the codes in which `lo` and `hi`, neighbours on the grid, differ: value j against the border
 // between them, border * d, by the sign of one fused multiply-add. The few values are read again (an
-// index into registers would put them all into local memory).
+// index into registers would put them all into local memory). A low unit is raised by a power of two, as
+// differences of its size would not be normal numbers.
 template <typename T>
 __device__ __forceinline__ uint32_t settle(uint32_t lo, uint32_t hi, const T* p, float d) {
+  const float by = d < 0x1p-60f ? 0x1p60f : 1.0f;
   for (uint32_t diff = lo ^ hi; diff != 0u;) {
     const int at = (__ffs(static_cast<int>(diff)) - 1) & ~3;
     const uint32_t c = (lo >> at) & 7u;
     // (grid[c] + grid[c + 1]) / 2: 1/4 + c/2 up to 7/4, then 5/2, 7/2, 5
     const float border = c < 4u ? 0.25f + 0.5f * static_cast<float>(c) : c < 6u ? static_cast<float>(c) - 1.5f : 5.0f;
-    const float s = fmaf(-border, d, fabsf(value_f32(p[at / 4])));
+    const float s = fmaf(-border, d * by, fabsf(value_f32(p[at / 4])) * by);
     if (s > 0.f || (s == 0.f && (c & 1u))) lo += 1u << at;
     diff &= ~(0xFu << at);
   }

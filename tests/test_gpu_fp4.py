@@ -131,6 +131,24 @@ def test_quantize_not_finite_and_extreme(fmt):
     _check_quant(big, fmt)
 
 
+@pytest.mark.parametrize("ts", [3.0e38, 1.0e38, 2.0 ** 61, 1.7e-18, 1.1e-30, 2.0 ** -118, 1.3e-38, 1e-41, 2.0 ** -149])
+def test_quantize_far_tensor_scales(ts):
+    # blocks whose scales run from 0 over the subnormal ones to the largest, where the values exist in 32 bits
+    g = _gen(17)
+    ts = torch.tensor([ts], dtype=torch.float32)
+    rows = []
+    for e in range(-14, 13):
+        amax = ts.double() * 2.0 ** e * (1 + torch.rand(1, generator=g).double())
+        rows.append((torch.rand(64, generator=g).double() * 2 - 1) * amax)
+    x = torch.stack(rows).clamp(-3.0e38, 3.0e38).float()
+    codes, scales = moe.quantize_fp4(x.cuda(), "nvfp4", ts.cuda())
+    rc, rs, _ = ref.quantize(x.double().numpy(), "nvfp4", ts.item())
+    assert np.array_equal(scales.cpu().numpy(), rs)
+    unit = (ref.E4M3[rs].astype(np.float32) * np.float32(ts.item())).repeat(8, 1)
+    rc = np.where(unit >= np.finfo(np.float32).tiny, rc, 0)     # a unit below the normal range: zeros
+    assert np.array_equal(codes.cpu().numpy(), rc)
+
+
 # ------------------------------------------------------------------ products
 def _weights(E, N, K, fmt, seed):
     w = torch.randn((E * N, K), generator=_gen(seed)) / K ** 0.5
