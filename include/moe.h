@@ -522,7 +522,7 @@ MOE_API moe_status moe_quantize_fp4(int32_t format, const void* src, int32_t dty
                                     int64_t row_stride, const float* tensor_scale, uint8_t* codes, uint8_t* scales,
                                     int64_t scale_stride, moe_stream_t stream);
 
-/* The values of codes and scales, rounded once to dst [rows, cols] (contiguous, dtype). */
+/* The values of codes and scales, e2m1 * d in fp32, rounded to dst [rows, cols] (contiguous, dtype). */
 MOE_API moe_status moe_dequantize_fp4(int32_t format, const uint8_t* codes, const uint8_t* scales, int64_t rows,
                                       int32_t cols, int64_t scale_stride, const float* tensor_scale, void* dst,
                                       int32_t dtype, moe_stream_t stream);
@@ -535,7 +535,8 @@ MOE_API moe_status moe_dequantize_fp4(int32_t format, const uint8_t* codes, cons
  *          behind a row's last scale is read. Where the call needs no workspace, base and
  *          stride are multiples of 8 (MXFP4) or 16 (NVFP4) bytes (moe_fp4_pad_scales makes such
  *          rows of others); otherwise any
- *   x_tensor_scale fp32 [1], w_tensor_scale fp32 [E] (device) or NULL; NVFP4 only
+ *   x_tensor_scale fp32 [1], w_tensor_scale fp32 [E] (device) or NULL; NVFP4 only. The product of
+ *          the two is taken in fp32, and has to be finite there
  *   offsets int32 [E + 1] device: rows offsets[g] .. offsets[g + 1] meet w[g]. Rows in none of
  *          these ranges (behind the last, in front of the first) are left as they were. Values are
  *          clamped to [0, T] and to ascending order. NULL: E = 1, every row.
@@ -578,7 +579,8 @@ MOE_API moe_status moe_fp4_matmul(const moe_fp4_product* p, moe_stream_t stream)
 /*
  * The same with x [T, K] in x_dtype (moe_value_dtype), rows x_row_stride elements apart, quantised
  * first (moe_quantize_fp4 with x_tensor_scale): p->x is x, p->x_scales and p->x_scale_stride are
- * not used, and the workspace has moe_fp4_linear_workspace_bytes(...) bytes (never 0 for T > 0).
+ * not used, and the workspace has moe_fp4_linear_workspace_bytes(...) bytes (never 0 for T > 0, but
+ * for shapes that are refused). T * K <= 2^33 here.
  */
 MOE_API int64_t moe_fp4_linear_workspace_bytes(int32_t format, int32_t T, int32_t N, int32_t K, int32_t E);
 MOE_API moe_status moe_fp4_linear(const moe_fp4_product* p, int32_t x_dtype, int64_t x_row_stride,

@@ -366,7 +366,7 @@ def quantize_fp4(x: torch.Tensor, fmt: str, tensor_scale: Optional[torch.Tensor]
 
 def dequantize_fp4(codes: torch.Tensor, scales: torch.Tensor, fmt: str, tensor_scale: Optional[torch.Tensor] = None,
                    dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
-    """The values [rows, K] that codes [rows, K/2] and scales stand for, rounded once to dtype."""
+    """The values [rows, K] that codes [rows, K/2] and scales stand for, in fp32, rounded to dtype."""
     if stream is not None:
         with _on_stream(stream):
             return dequantize_fp4(codes, scales, fmt, tensor_scale, dtype)

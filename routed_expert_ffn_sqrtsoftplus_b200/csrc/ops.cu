@@ -17,6 +17,9 @@ cudaStream_t as_stream(moe_stream_t s) { return reinterpret_cast<cudaStream_t>(s
 
 bool aligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
+// Values that the quantisers take in one call (they count runs in 32 bits).
+constexpr int64_t kMaxQuantized = int64_t(1) << 33;
+
 int value_bytes(int32_t dtype) {
   return dtype == MOE_VAL_FP32 ? 4 : dtype == MOE_VAL_BF16 || dtype == MOE_VAL_FP16 ? 2 : 0;
 }
@@ -203,7 +206,7 @@ moe_status moe_quantize_fp4(int32_t format, const void* src, int32_t dtype, int6
     return MOE_ERR_INVALID_ARG;
   if (scale_stride < cols / (format == MOE_FP4_NV ? 16 : 32)) return MOE_ERR_INVALID_ARG;
   if (format == MOE_FP4_MX && tensor_scale != nullptr) return MOE_ERR_INVALID_ARG;
-  if (rows > (int64_t(1) << 33) / cols) return MOE_ERR_UNSUPPORTED;
+  if (rows > kMaxQuantized / cols) return MOE_ERR_UNSUPPORTED;
   if (rows == 0) return MOE_OK;
   if (src == nullptr || codes == nullptr || scales == nullptr) return MOE_ERR_INVALID_ARG;
   if (!aligned(src, vb) || !aligned(codes, 16) || !aligned(tensor_scale, 4)) return MOE_ERR_INVALID_ARG;
@@ -220,7 +223,7 @@ moe_status moe_dequantize_fp4(int32_t format, const uint8_t* codes, const uint8_
   if (!fp4_format_ok(format) || vb == 0 || rows < 0 || cols <= 0 || cols % 32 != 0) return MOE_ERR_INVALID_ARG;
   if (scale_stride < cols / (format == MOE_FP4_NV ? 16 : 32)) return MOE_ERR_INVALID_ARG;
   if (format == MOE_FP4_MX && tensor_scale != nullptr) return MOE_ERR_INVALID_ARG;
-  if (rows > (int64_t(1) << 33) / cols) return MOE_ERR_UNSUPPORTED;
+  if (rows > kMaxQuantized / cols) return MOE_ERR_UNSUPPORTED;
   if (rows == 0) return MOE_OK;
   if (codes == nullptr || scales == nullptr || dst == nullptr) return MOE_ERR_INVALID_ARG;
   if (!aligned(codes, 16) || !aligned(dst, vb) || !aligned(tensor_scale, 4)) return MOE_ERR_INVALID_ARG;
@@ -263,7 +266,8 @@ moe_status moe_fp4_matmul(const moe_fp4_product* p, moe_stream_t stream) {
 }
 
 int64_t moe_fp4_linear_workspace_bytes(int32_t format, int32_t T, int32_t N, int32_t K, int32_t E) {
-  if (!fp4_format_ok(format) || !product_shape_ok(T, N, K, E) || K % 32 != 0 || T == 0) return 0;
+  if (!fp4_format_ok(format) || !product_shape_ok(T, N, K, E) || K % 32 != 0 || T == 0 || T > kMaxQuantized / K)
+    return 0;
   return T * (K / 2 + padded_scales(format, K)) + moe_fp4_workspace_bytes(format, T, N, K, E);
 }
 
@@ -271,6 +275,7 @@ moe_status moe_fp4_linear(const moe_fp4_product* p, int32_t x_dtype, int64_t x_r
   if (p == nullptr) return MOE_ERR_INVALID_ARG;
   moe_status st = check_product(*p);
   if (st != MOE_OK || p->T == 0) return st;
+  if (p->T > kMaxQuantized / p->K) return MOE_ERR_UNSUPPORTED;
   const int vb = value_bytes(x_dtype);
   if (vb == 0 || x_row_stride < p->K || p->x == nullptr || !aligned(p->x, vb) || p->x == p->y ||
       p->workspace == nullptr)

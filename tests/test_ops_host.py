@@ -117,6 +117,9 @@ def test_fp4_linear_refuses_bad_arguments(L):
     assert f(dt=3) == INV and f(rs=63) == INV and f(x=FAKE + 1) == INV and f(x=None) == INV
     assert f(workspace=None) == INV and f(workspace_bytes=4 * 48 - 1) == INV and f(workspace=FAKE + 8) == INV
     assert L.moe_fp4_linear(None, 0, 64, None) == INV and f(T=0) == OK
+    # the quantiser counts in 32 bits: 2^33 values a call
+    assert f(T=1 << 20, K=1 << 14, w_scale_stride=1 << 10, rs=1 << 14) == UNS
+    assert w(0, 1 << 20, 64, 1 << 14, 1) == 0 and w(0, 1 << 19, 64, 1 << 14, 1) > 0
 
 
 def test_bindings_refuse_bad_tensors(L):
