@@ -230,11 +230,32 @@ def _current(t: torch.Tensor) -> int:
     return torch._C._cuda_getCurrentRawStream(t.device.index)
 
 
-def _same_device(ref: torch.Tensor, **tensors):
-    dev = ref.device
-    for n, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{n} is on {t.device}, expected {dev}")
+# A call's time on few rows is the host's: an output through new_empty takes 1.9 us of it, through the
+# allocator's own entry 0.8 (on the current device, where the library wants every tensor to be).
+try:
+    from torch._C._dynamo.guards import _empty_strided_cuda
+except ImportError:
+    _empty_strided_cuda = None
+
+
+def _empty(ref: torch.Tensor, rows: int, cols: int, dtype) -> torch.Tensor:
+    """A matrix for a call's results, on ref's device."""
+    if _empty_strided_cuda is None or ref.get_device() != torch._C._cuda_getDevice():
+        return ref.new_empty((rows, cols), dtype=dtype)
+    return _empty_strided_cuda((rows, cols), (cols, 1), dtype)
+
+
+def _bytes(ref: torch.Tensor, n: int) -> torch.Tensor:
+    """A workspace of n bytes."""
+    return _empty(ref, 1, n, torch.uint8)
+
+
+def _arg(t: torch.Tensor, name: str, dtype, shape, ref: torch.Tensor):
+    """A contiguous tensor of this type and shape (None: any), on ref's device."""
+    if t.dtype != dtype or t.get_device() != ref.get_device() or not t.is_contiguous() or (
+            shape is not None and t.shape != shape):
+        _need(t, name, dtype, shape, ref.device.type)
+        raise ValueError(f"{name} is on {t.device}, expected {ref.device}")
 
 
 def _rows(t: torch.Tensor, name: str):
@@ -247,6 +268,8 @@ def _rows(t: torch.Tensor, name: str):
     if t.dim() != 2:
         raise ValueError(f"{name} must have 2 dimensions, got {t.dim()}")
     (r, c), (rs, cs) = t.shape, t.stride()
+    if r >= 1 << 31 or c >= 1 << 31:
+        raise ValueError(f"{name} must have fewer than 2^31 rows and columns")
     if c > 1 and cs != 1:
         raise ValueError(f"{name} must have contiguous rows")
     if r <= 1:
@@ -262,6 +285,8 @@ def _route_config(E, k, n_groups, topk_groups, score, group_score, renormalize, 
         raise ValueError(f"score must be one of {tuple(SCORES)}")
     if group_score not in ("top2", "max"):
         raise ValueError("group_score must be 'top2' or 'max'")
+    if not 1 <= k <= E or max(n_groups, topk_groups) >= 1 << 31:
+        raise ValueError(f"top_k must be 1 .. {E}, got {k}, with fewer than 2^31 groups")
     return _RouteConfig(E, k, n_groups, topk_groups, SCORES[score], group_score == "top2", bool(renormalize),
                         route_scale)
 
@@ -285,17 +310,16 @@ def route(logits: torch.Tensor, top_k: int, *, score: str = "softmax", bias: Opt
                          topk_idx=topk_idx, topk_w=topk_w)
     T, E, rs, code = _rows(logits, "logits")
     if bias is not None:
-        _need(bias, "bias", torch.float32, (E,))
+        _arg(bias, "bias", torch.float32, (E,), logits)
     cfg = _route_config(E, top_k, n_groups, topk_groups, score, group_score, renormalize, route_scale)
     if topk_idx is None:
-        topk_idx = logits.new_empty((T, top_k), dtype=torch.int32)
+        topk_idx = _empty(logits, T, top_k, torch.int32)
     else:
-        _need(topk_idx, "topk_idx", torch.int32, (T, top_k))
+        _arg(topk_idx, "topk_idx", torch.int32, (T, top_k), logits)
     if topk_w is None:
-        topk_w = logits.new_empty((T, top_k), dtype=torch.float32)
+        topk_w = _empty(logits, T, top_k, torch.float32)
     else:
-        _need(topk_w, "topk_w", torch.float32, (T, top_k))
-    _same_device(logits, bias=bias, topk_idx=topk_idx, topk_w=topk_w)
+        _arg(topk_w, "topk_w", torch.float32, (T, top_k), logits)
     _check(lib().moe_route(cfg, logits.data_ptr(), code, rs, _addr(bias), T, topk_idx.data_ptr(),
                            topk_w.data_ptr(), _current(logits)), "moe_route")
     return topk_idx, topk_w
@@ -311,14 +335,13 @@ def route_backward(grad_w: torch.Tensor, logits: torch.Tensor, topk_idx: torch.T
                                   route_scale=route_scale, out=out)
     T, E, rs, code = _rows(logits, "logits")
     k = topk_idx.shape[-1]
-    _need(topk_idx, "topk_idx", torch.int32, (T, k))
-    _need(grad_w, "grad_w", torch.float32, (T, k))
+    _arg(topk_idx, "topk_idx", torch.int32, (T, k), logits)
+    _arg(grad_w, "grad_w", torch.float32, (T, k), logits)
     cfg = _route_config(E, k, 1, 1, score, "max", renormalize, route_scale)
     if out is None:
-        out = logits.new_empty((T, E))
+        out = _empty(logits, T, E, logits.dtype)
     else:
-        _need(out, "out", logits.dtype, (T, E))
-    _same_device(logits, grad_w=grad_w, topk_idx=topk_idx, out=out)
+        _arg(out, "out", logits.dtype, (T, E), logits)
     _check(lib().moe_route_backward(cfg, grad_w.data_ptr(), logits.data_ptr(), code, rs, topk_idx.data_ptr(), T,
                                     out.data_ptr(), _current(logits)), "moe_route_backward")
     return out
@@ -330,14 +353,14 @@ def _fp4_format(fmt: str) -> int:
     return FP4_FORMATS[fmt]
 
 
-def _tensor_scale(t: Optional[torch.Tensor], name: str, fmt: str, n: int):
+def _tensor_scale(t: Optional[torch.Tensor], name: str, fmt: str, n: int, ref: torch.Tensor):
     if t is None:
         return None
     if fmt != "nvfp4":
         raise ValueError(f"{name} is for nvfp4")
     if t.numel() != n:
         raise ValueError(f"{name} must hold {n} value(s), got {t.numel()}")
-    _need(t, name, torch.float32)
+    _arg(t, name, torch.float32, None, ref)
     return t.data_ptr()
 
 
@@ -354,11 +377,10 @@ def quantize_fp4(x: torch.Tensor, fmt: str, tensor_scale: Optional[torch.Tensor]
     rows, K, rs, code = _rows(x, "x")
     if K % 32 != 0:
         raise ValueError(f"x must have a multiple of 32 columns, got {K}")
-    ts = _tensor_scale(tensor_scale, "tensor_scale", fmt, 1)
-    _same_device(x, tensor_scale=tensor_scale)
+    ts = _tensor_scale(tensor_scale, "tensor_scale", fmt, 1, x)
     sc = K // FP4_BLOCK[fmt]
-    codes = x.new_empty((rows, K // 2), dtype=torch.uint8)
-    scales = x.new_empty((rows, sc), dtype=torch.uint8)
+    codes = _empty(x, rows, K // 2, torch.uint8)
+    scales = _empty(x, rows, sc, torch.uint8)
     _check(lib().moe_quantize_fp4(f, x.data_ptr(), code, rows, K, rs, ts, codes.data_ptr(), scales.data_ptr(), sc,
                                   _current(x)), "moe_quantize_fp4")
     return codes, scales
@@ -377,36 +399,37 @@ def dequantize_fp4(codes: torch.Tensor, scales: torch.Tensor, fmt: str, tensor_s
         raise ValueError(f"codes must have 2 dimensions, got {codes.dim()}")
     rows, K = codes.shape[0], codes.shape[1] * 2
     _need(codes, "codes", torch.uint8)
+    if K >= 1 << 31:
+        raise ValueError("codes must have fewer than 2^30 columns")
     if K % 32 != 0:
         raise ValueError(f"codes must have a multiple of 16 columns, got {codes.shape[1]}")
-    _need(scales, "scales", torch.uint8, (rows, K // FP4_BLOCK[fmt]))
-    ts = _tensor_scale(tensor_scale, "tensor_scale", fmt, 1)
-    _same_device(codes, scales=scales, tensor_scale=tensor_scale)
-    out = codes.new_empty((rows, K), dtype=dtype)
+    _arg(scales, "scales", torch.uint8, (rows, K // FP4_BLOCK[fmt]), codes)
+    ts = _tensor_scale(tensor_scale, "tensor_scale", fmt, 1, codes)
+    out = _empty(codes, rows, K, dtype)
     _check(lib().moe_dequantize_fp4(f, codes.data_ptr(), scales.data_ptr(), rows, K, scales.shape[1], ts,
                                     out.data_ptr(), _VALUE_DTYPES[dtype], _current(codes)), "moe_dequantize_fp4")
     return out
 
 
-def _fp4_weights(w, w_scales, fmt, K, offsets):
+def _fp4_weights(w, w_scales, fmt, K, offsets, ref):
     """(E, N) of w [N, K/2] or, with offsets, [E, N, K/2]."""
     lead = w.shape[:-1]
     if w.dim() != (2 if offsets is None else 3) or w.shape[-1] * 2 != K:
         raise ValueError(f"w must be [{'' if offsets is None else 'E, '}N, {K // 2}], got {tuple(w.shape)}")
-    _need(w, "w", torch.uint8)
-    _need(w_scales, "w_scales", torch.uint8, tuple(lead) + (K // FP4_BLOCK[fmt],))
-    E = 1 if offsets is None else w.shape[0]
-    if offsets is not None:
-        _need(offsets, "offsets", torch.int32, (E + 1,))
-    return E, lead[-1]
+    _arg(w, "w", torch.uint8, None, ref)
+    _arg(w_scales, "w_scales", torch.uint8, lead + (K // FP4_BLOCK[fmt],), ref)
+    if offsets is None:
+        return 1, lead[0]
+    _arg(offsets, "offsets", torch.int32, (lead[0] + 1,), ref)
+    return lead
 
 
 def _fp4_out(x, T, N, out, out_dtype):
     if out is None:
-        return x.new_empty((T, N), dtype=out_dtype)
+        return _empty(x, T, N, out_dtype)
     if out.dtype not in _VALUE_DTYPES:
         raise ValueError(f"out must be bfloat16, float16 or float32, got {out.dtype}")
-    _need(out, "out", out.dtype, (T, N))
+    _arg(out, "out", out.dtype, (T, N), x)
     return out
 
 
@@ -424,6 +447,8 @@ def _aligned_scales(scales, f):
 
 @functools.lru_cache(maxsize=4096)
 def _fp4_workspace_bytes(linear, device, *shape):
+    if max(shape) >= 1 << 31:
+        raise ValueError("an FP4 product takes fewer than 2^31 rows, columns and experts")
     L = lib()
     return (L.moe_fp4_linear_workspace_bytes if linear else L.moe_fp4_workspace_bytes)(*shape)
 
@@ -453,24 +478,22 @@ def fp4_matmul(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_scale
     _need(x, "x", torch.uint8)
     if K % 32 != 0:
         raise ValueError(f"x must have a multiple of 16 columns, got {x.shape[1]}")
-    _need(x_scales, "x_scales", torch.uint8, (T, K // FP4_BLOCK[fmt]))
-    E, N = _fp4_weights(w, w_scales, fmt, K, offsets)
-    x_ts = _tensor_scale(x_tensor_scale, "x_tensor_scale", fmt, 1)
-    w_ts = _tensor_scale(w_tensor_scale, "w_tensor_scale", fmt, E)
+    _arg(x_scales, "x_scales", torch.uint8, (T, K // FP4_BLOCK[fmt]), x)
+    E, N = _fp4_weights(w, w_scales, fmt, K, offsets, x)
+    x_ts = _tensor_scale(x_tensor_scale, "x_tensor_scale", fmt, 1, x)
+    w_ts = _tensor_scale(w_tensor_scale, "w_tensor_scale", fmt, E, x)
     out = _fp4_out(x, T, N, out, out_dtype)
     if status is not None:
-        _need(status, "status", torch.int32, (1,))
-    _same_device(x, x_scales=x_scales, w=w, w_scales=w_scales, x_tensor_scale=x_tensor_scale,
-                 w_tensor_scale=w_tensor_scale, offsets=offsets, out=out, status=status)
+        _arg(status, "status", torch.int32, (1,), x)
     xss, wss = x_scales.shape[1], w_scales.shape[-1]
     nbytes = _fp4_workspace_bytes(False, x.device.index, f, T, N, K, E)
     if nbytes == 0:       # the scales are read as they are: aligned rows
         w_scales, wss = _aligned_scales(w_scales, f)
         x_scales, xss = _aligned_scales(x_scales, f)
-    space = w.new_empty(nbytes)
+    space = _bytes(x, nbytes) if nbytes else None
     p = _Fp4Product(f, T, N, K, E, _VALUE_DTYPES[out.dtype], x.data_ptr(), x_scales.data_ptr(), xss, x_ts,
-                    w.data_ptr(), w_scales.data_ptr(), wss, w_ts, _addr(offsets), out.data_ptr(),
-                    space.data_ptr() if nbytes else None, nbytes, _addr(status))
+                    w.data_ptr(), w_scales.data_ptr(), wss, w_ts, _addr(offsets), out.data_ptr(), _addr(space), nbytes,
+                    _addr(status))
     _check(lib().moe_fp4_matmul(p, _current(x)), "moe_fp4_matmul")
     return out
 
@@ -491,19 +514,17 @@ def fp4_linear(x: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor, fmt: st
     T, K, rs, code = _rows(x, "x")
     if K % 32 != 0:
         raise ValueError(f"x must have a multiple of 32 columns, got {K}")
-    E, N = _fp4_weights(w, w_scales, fmt, K, offsets)
-    x_ts = _tensor_scale(x_tensor_scale, "x_tensor_scale", fmt, 1)
-    w_ts = _tensor_scale(w_tensor_scale, "w_tensor_scale", fmt, E)
+    E, N = _fp4_weights(w, w_scales, fmt, K, offsets, x)
+    x_ts = _tensor_scale(x_tensor_scale, "x_tensor_scale", fmt, 1, x)
+    w_ts = _tensor_scale(w_tensor_scale, "w_tensor_scale", fmt, E, x)
     out = _fp4_out(x, T, N, out, x.dtype)
     if status is not None:
-        _need(status, "status", torch.int32, (1,))
-    _same_device(x, w=w, w_scales=w_scales, x_tensor_scale=x_tensor_scale, w_tensor_scale=w_tensor_scale,
-                 offsets=offsets, out=out, status=status)
+        _arg(status, "status", torch.int32, (1,), x)
     wss = w_scales.shape[-1]
     if _fp4_workspace_bytes(False, x.device.index, f, T, N, K, E) == 0:   # the scales are read as they are
         w_scales, wss = _aligned_scales(w_scales, f)
     nbytes = _fp4_workspace_bytes(True, x.device.index, f, T, N, K, E)
-    space = w.new_empty(nbytes)
+    space = _bytes(x, nbytes)
     p = _Fp4Product(f, T, N, K, E, _VALUE_DTYPES[out.dtype], x.data_ptr(), None, 0, x_ts, w.data_ptr(),
                     w_scales.data_ptr(), wss, w_ts, _addr(offsets), out.data_ptr(), space.data_ptr(), nbytes,
                     _addr(status))

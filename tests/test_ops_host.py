@@ -170,3 +170,24 @@ def test_structs_match_the_header():
         body = re.sub(r"/\*.*?\*/", "", body, flags=re.S)
         fields = [f.strip(" *\n") for line in body.split(";") for f in re.sub(r"^\s*(const )?\w+", "", line).split(",")]
         assert [f for f in fields if f] == [n for n, _ in cls._fields_]
+
+
+def test_bindings_refuse_sizes_that_32_bits_do_not_hold(L):
+    for args in ((8, 0, 1, 1), (8, -1, 1, 1), (8, 9, 1, 1), (8, (1 << 32) + 2, 1, 1), (8, 2, 1 << 32, 1)):
+        with pytest.raises(ValueError):
+            moe._route_config(*args, "softmax", "max", True, 1.0)
+    with pytest.raises(ValueError):
+        moe._fp4_workspace_bytes(False, 0, 0, (1 << 32) + 4, 64, 64, 1)
+    # CUDA tensors as far as the checks ask, without their memory
+    class Rows:
+        is_cuda, dtype = True, torch.float32
+        def __init__(self, *shape):
+            self.shape = shape
+        def dim(self):
+            return 2
+        def stride(self):
+            return self.shape[1], 1
+    assert moe._rows(Rows(3, 8), "x") == (3, 8, 8, 2)
+    for shape in ((1 << 31, 8), ((1 << 32) + 3, 1), (1, 1 << 31)):
+        with pytest.raises(ValueError):
+            moe._rows(Rows(*shape), "x")
