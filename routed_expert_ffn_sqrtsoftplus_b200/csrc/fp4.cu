@@ -146,13 +146,17 @@ __device__ __forceinline__ int e4m3_scale(float amax, float ts) {
 // Eight scaled values to a word of E2M1 codes, the first in the lowest nibble: nearest, ties to even, at most 6.
 __device__ __forceinline__ uint32_t to_e2m1x8(const float* v, float scale) {
   uint32_t r;
-  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t.reg .b64 s, p, q, r, t;\n\t.reg .f32 x, y;\n\t"
+      "mov.b64 s, {%9, %9};\n\tmov.b64 p, {%1, %2};\n\tmov.b64 q, {%3, %4};\n\t"
+      "mov.b64 r, {%5, %6};\n\tmov.b64 t, {%7, %8};\n\t"
+      "mul.rn.f32x2 p, p, s;\n\tmul.rn.f32x2 q, q, s;\n\tmul.rn.f32x2 r, r, s;\n\tmul.rn.f32x2 t, t, s;\n\t"
+      "mov.b64 {x, y}, p;\n\tcvt.rn.satfinite.e2m1x2.f32 a, y, x;\n\t"
+      "mov.b64 {x, y}, q;\n\tcvt.rn.satfinite.e2m1x2.f32 b, y, x;\n\t"
+      "mov.b64 {x, y}, r;\n\tcvt.rn.satfinite.e2m1x2.f32 c, y, x;\n\t"
+      "mov.b64 {x, y}, t;\n\tcvt.rn.satfinite.e2m1x2.f32 d, y, x;\n\t"
       "mov.b32 %0, {a, b, c, d};\n\t}\n"
       : "=r"(r)
-      : "f"(v[0] * scale), "f"(v[1] * scale), "f"(v[2] * scale), "f"(v[3] * scale), "f"(v[4] * scale),
-        "f"(v[5] * scale), "f"(v[6] * scale), "f"(v[7] * scale));
+      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(scale));
   return r;
 }
 

@@ -873,35 +873,51 @@ cudaError_t launch_cfg(const CUtensorMap& tw, const CUtensorMap& tx, const Fp4Ge
 // Scales into the MMA's order: for each tile (of kCols rows of w, or of kTokens rows of x) and each K
 // block of 256, 128-row blocks of kNv ? 4 : 2 words, each word 512 bytes with row r at 16 (r % 32) +
 // 4 (r / 32); zeros for rows outside the tile and behind a row's end. Blocks x: the tiles of w, expert
-// by expert, then those of x; y: four K blocks each. A thread writes 16 bytes.
+// by expert, then those of x; y: 64 bytes of every row. A thread takes 16 bytes of rows l, l + 32, l + 64
+// and l + 96, a neighbour the next 16: a 4 x 4 matrix of words, whose columns are the 16-byte pieces.
+constexpr int kArrangeBytes = 64;
+// A row's 16 bytes at c, zeros from n on.
+__device__ __forceinline__ uint4 scale_words(const uint8_t* row, int c, int n, int align) {
+  const uint8_t* s = row + c;
+  if (align >= 16 && c + 16 <= n) return __ldg(reinterpret_cast<const uint4*>(s));
+  uint32_t w[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    w[j] = 0u;
+    if (align >= 4 && c + 4 * j + 4 <= n) {
+      w[j] = __ldg(reinterpret_cast<const uint32_t*>(s + 4 * j));
+    } else {
+      for (int e = 0; e < 4; ++e)
+        if (c + 4 * j + e < n) w[j] |= static_cast<uint32_t>(__ldg(s + 4 * j + e)) << (8 * e);
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
 template <bool kNv, int kRows>
 __device__ __forceinline__ void arrange_tile(const uint8_t* src, int64_t stride, int rows, int sf_cols, int num_kb,
                                              uint4* out) {
-  constexpr int kWords = kNv ? 4 : 2, kBlocks = (kRows + 127) / 128, kSf = kNv ? 16 : 8;
-  constexpr int kPerKb = kBlocks * kWords * 32;  // 16-byte pieces of a K block
-  const bool words = (reinterpret_cast<uintptr_t>(src) | stride) % 4 == 0;
-  const int kb0 = blockIdx.y * 4, n = min(4, num_kb - kb0) * kPerKb;
-  for (int i = threadIdx.x; i < n; i += blockDim.x) {
-    const int kb = kb0 + i / kPerKb, p = i % kPerKb;
-    // neighbouring threads take a row's words, so that a row's bytes are read together
-    const int j = p % kWords, l = p / kWords % 32, b = p / (kWords * 32);
-    const int c = kb * kSf + j * 4;
-    uint32_t w[4];
+  constexpr int kWords = kNv ? 4 : 2, kBlocks = (kRows + 127) / 128;
+  const uint64_t at = reinterpret_cast<uintptr_t>(src) | static_cast<uint64_t>(stride);
+  const int align = at % 16 == 0 ? 16 : at % 4 == 0 ? 4 : 1;
+  for (int i = threadIdx.x; i < kArrangeBytes / 16 * kBlocks * 32; i += blockDim.x) {
+    const int l = i / 2 % 32, b = i / 64 % kBlocks;
+    const int c = blockIdx.y * kArrangeBytes + (i % 2 + i / (64 * kBlocks) * 2) * 16;
+    uint4 v[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int r = b * 128 + q * 32 + l;
-      w[q] = 0u;
-      if (r < rows && c < sf_cols) {
-        const uint8_t* s = src + static_cast<int64_t>(r) * stride + c;
-        if (words && c + 4 <= sf_cols) {
-          w[q] = __ldg(reinterpret_cast<const uint32_t*>(s));
-        } else {
-          for (int e = 0; e < 4; ++e)
-            if (c + e < sf_cols) w[q] |= static_cast<uint32_t>(__ldg(s + e)) << (8 * e);
-        }
-      }
+      v[q] = make_uint4(0u, 0u, 0u, 0u);
+      if (r < rows && c < sf_cols) v[q] = scale_words(src + static_cast<int64_t>(r) * stride, c, sf_cols, align);
     }
-    out[static_cast<int64_t>(kb) * kPerKb + (b * kWords + j) * 32 + l] = make_uint4(w[0], w[1], w[2], w[3]);
+    // words c / 4 .. c / 4 + 3 of a row: K block, word in it
+    const uint32_t* w[4] = {&v[0].x, &v[1].x, &v[2].x, &v[3].x};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int kb = c / (4 * kWords) + j / kWords;
+      if (kb < num_kb)
+        out[(static_cast<int64_t>(kb) * kBlocks * kWords + b * kWords + j % kWords) * 32 + l] =
+            make_uint4(w[0][j], w[1][j], w[2][j], w[3][j]);
+    }
   }
 }
 
@@ -910,12 +926,11 @@ __global__ void __launch_bounds__(256) arrange_scales_kernel(const Fp4GemmArgs a
   constexpr int kWords = kNv ? 4 : 2;
   __shared__ int pre[kMaxExperts + 1], row_s[kMaxExperts + 1];
   wait_for_previous_kernel();
-  if (threadIdx.x < 32) scan_experts<kTokens>(a.offsets, a.E, a.T, pre, row_s);
-  __syncthreads();
   int tile = blockIdx.x;
   if (tile < a.E * a.m_tiles) {
     const int g = tile / a.m_tiles, m = tile - g * a.m_tiles;
-    if (row_s[g] == row_s[g + 1]) return;  // no row meets this expert
+    // no row meets this expert (in whatever order the offsets are: rows of g are rows behind all before it)
+    if (a.offsets && min(a.T, __ldg(a.offsets + g + 1)) <= max(0, __ldg(a.offsets + g))) return;
     const int rows = min(kCols, a.N - m * kCols);
     arrange_tile<kNv, kCols>(a.ws + (static_cast<int64_t>(g) * a.N + m * kCols) * a.ws_stride, a.ws_stride, rows,
                              a.sf_cols, a.num_kb,
@@ -924,6 +939,8 @@ __global__ void __launch_bounds__(256) arrange_scales_kernel(const Fp4GemmArgs a
     return;
   }
   tile -= a.E * a.m_tiles;
+  if (threadIdx.x < 32) scan_experts<kTokens>(a.offsets, a.E, a.T, pre, row_s);
+  __syncthreads();
   if (tile >= pre[a.E]) return;
   int lo = 0, hi = a.E - 1;
   while (lo < hi) {
@@ -939,7 +956,7 @@ __global__ void __launch_bounds__(256) arrange_scales_kernel(const Fp4GemmArgs a
 
 template <bool kNv, int kTokens, int kCols>
 cudaError_t launch_arrange(const Fp4GemmArgs& a, int64_t xtiles, cudaStream_t s) {
-  const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(a.E) * a.m_tiles + xtiles), (a.num_kb + 3) / 4);
+  const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(a.E) * a.m_tiles + xtiles), (a.num_kb * (kNv ? 16 : 8) + kArrangeBytes - 1) / kArrangeBytes);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(256);
