@@ -22,7 +22,9 @@
 // with more than 32 of either is selected from 64-bit keys as a whole (select_row_f64). So the
 // result is always that of the 64-bit keys.
 //
-// Bound by the selection's instructions: some 550 a row, where the row is 1 KB.
+// Bound by instructions: 1090 a row of 256 FP32 logits with bias and groups (13.0 us for 8192 rows, of which HBM
+// needs 1.3; 2.5 of 4 issue slots are taken while the SMs are busy, and a row in itself takes 3 us of latencies), 560
+// a row of 128 BF16 logits without either (4.2 us for 4099 rows; HBM 0.2).
 #include <cuda_fp16.h>
 
 #include "common.cuh"
@@ -345,30 +347,46 @@ __device__ __forceinline__ int select_by_rounds(uint32_t (&key)[EPL], int e0, in
   return n;
 }
 
-// By a list: the k-th largest of the lanes' maxima bounds the k-th largest key from below, and few keys
-// reach that bound. They go to a list of at most 32 (key, expert), one a lane, and each counts those ahead of
+// By a list: the k-th largest of the lanes' maxima (with 12 keys a lane or more, of their halves' maxima)
+// bounds the k-th largest key from below, and few keys reach that bound. They go to a list of at most 32 (key, expert), one a lane, and each counts those ahead of
 // it. -1 where there are more; `tol` lowers the bound, so that the list also holds what
 // floats cannot tell from the last slot. Some 200 instructions where rounds take 60 each.
-constexpr int kListK = 16;  // above, the bound lets too many through (half the lanes: 22 on average)
+//
+// Halves where they are long: of 512 experts in 8 groups, 4 of them kept, 16 lanes are live, and a list for 16
+// slots by their maxima is the 256 keys of them all (16384 rows in rounds: 72.6 us, by halves 46.9; by halves
+// without groups, 12 slots, 26.5 against 25.6). Above 16 slots the bound lets too many through either way.
+constexpr int kListK = 16;
 template <int EPL>
 __device__ __forceinline__ int select_by_list(const uint32_t (&key)[EPL], int e0, int k, float tol, uint2* list,
                                               int lane, int& mine, uint32_t& mkey, uint32_t& left) {
-  uint32_t bk = 0u;
+  constexpr int kParts = EPL >= 12 ? 2 : 1, kLen = EPL / kParts;
+  uint32_t bk[kParts];
+  int live = 0;
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) bk = max(bk, key[i]);
-  // the k-th maximum of few more than k lanes (the others' groups are out) is a low one: the list would
-  // overflow (of 4 k / 3 lanes with 16 keys each some 21 reach it, of k lanes all)
-  const int live = __popc(__ballot_sync(kFull, bk != 0u));
-  if (4 * k > 3 * live && live * EPL > 32) return -1;
+  for (int h = 0; h < kParts; ++h) {
+    bk[h] = 0u;
+#pragma unroll
+    for (int i = 0; i < kLen; ++i) bk[h] = max(bk[h], key[h * kLen + i]);
+    live += __popc(__ballot_sync(kFull, bk[h] != 0u));
+  }
+  // the k-th maximum of few more than k parts (the others' groups are out) is a low one: the list would
+  // overflow (of 4 k / 3 parts with 16 keys each some 21 reach it, of k parts all)
+  if (4 * k > 3 * live && live * kLen > 32) return -1;
   uint32_t bound = 0u;
   int reached = 0;
   for (int r = 0; r < k && reached < k; ++r) {  // equal maxima go together
-    bound = __reduce_max_sync(kFull, bk);
-    const bool top = bk == bound;
-    reached += __popc(__ballot_sync(kFull, top));
-    if (top) bk = 0u;
+    uint32_t most = bk[0];
+#pragma unroll
+    for (int h = 1; h < kParts; ++h) most = max(most, bk[h]);
+    bound = __reduce_max_sync(kFull, most);
+#pragma unroll
+    for (int h = 0; h < kParts; ++h) {
+      const bool top = bk[h] == bound;
+      reached += __popc(__ballot_sync(kFull, top));
+      if (top) bk[h] = 0u;
+    }
   }
-  // fewer than k lanes with live experts: everything live
+  // fewer than k parts with live experts: everything live
   if (reached < k || bound == 0u) bound = 1u;
   if (tol > 0.f && bound > 1u) {
     const float f = value_of(bound);
@@ -489,15 +507,17 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
       merge(a.lane_shift);
     } else {
       float* fb = reinterpret_cast<float*>(key_buf + static_cast<size_t>(warp) * a.E);  // this warp's alone
+      // lanes EPL apart, each on a bank of its own (16384 x 480, 8 groups: 50.2 us, 56.9 without)
+      auto pad = [](int e) { return e + (e >> 4); };
 #pragma unroll
       for (int i = 0; i < EPL; ++i)
-        if (e0 + i < a.E) fb[e0 + i] = v[i];
+        if (e0 + i < a.E) fb[pad(e0 + i)] = v[i];
       __syncwarp();
       // 2^scan_shift lanes scan a group
       const int g = lane >> a.scan_shift, step = 1 << a.scan_shift;
       if (g < a.G)
         for (int j = lane & (step - 1); j < Eg; j += step) {
-          const float x = fb[g * Eg + j];
+          const float x = fb[pad(g * Eg + j)];
           w2 = fmaxf(w2, fminf(w1, x));
           w1 = fmaxf(w1, x);
         }
@@ -615,7 +635,8 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
 //                 softmax       dz_e = s_e (scale g_e [e selected] - scale sum_j g_j s_j), every e
 // One warp per row; lane r holds slot r (an expert named twice adds up). The row is written 16 bytes a
 // lane without the slots' own terms (zeros, or in the dense form -s_e scale sum_j g_j s_j from a row held
-// in registers), and the slots' elements go over it: one warp, so in this order. Bound by HBM's writes.
+// in registers), and the slots' elements go over it: one warp, so in this order. Bound by HBM's writes: 16384 x
+// 512 FP32, 16 slots, 9.6 us (HBM 5.6), dense 13.5 (10.6; 39 with the row read and exponentiated twice).
 template <typename T, bool kDense>
 __global__ void __launch_bounds__(kRouteWarps * 32)
     route_grad_kernel(const float* __restrict__ grad_w, const T* __restrict__ logits, int64_t row_stride,
