@@ -111,14 +111,12 @@ __device__ __forceinline__ bool unpack(const Raw<__half>& r, float (&v)[kRun], f
 }
 
 // E4M3 value of a non-negative code (0 .. 126).
-__device__ __forceinline__ float e4m3_value(int code) {
-  const int e = code >> 3, m = code & 7;
-  return e == 0 ? static_cast<float>(m) * 0.001953125f
-                : __uint_as_float(static_cast<uint32_t>(e + 120) << 23 | static_cast<uint32_t>(m) << 20);
+__device__ __forceinline__ float e4m3_value(uint32_t code) {
+  return __half2float(__half(__nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(code), __NV_E4M3)));
 }
 
 // The E4M3 code nearest to amax / (6 ts), ties to even, at most 126 (448).
-__device__ __forceinline__ int e4m3_scale(float amax, float ts) {
+__device__ __forceinline__ uint32_t e4m3_scale(float amax, float ts) {
   // far out, both by one power of two, so that neither the reciprocal nor a difference leaves the normal range
   // (where amax does, the code is 0 or 126 with or without it)
   if (ts < 0x1p-60f || ts > 0x1p60f) {
@@ -126,19 +124,17 @@ __device__ __forceinline__ int e4m3_scale(float amax, float ts) {
     ts *= by;
     amax *= by;
   }
-  const float q = amax * __frcp_rn(6.0f * ts);  // off by a few units of 2^-24: the code is right, or a neighbour
-  int c = static_cast<int>(__nv_cvt_float_to_fp8(q, __NV_SATFINITE, __NV_E4M3)) & 0x7F;
-  c = min(c, 126);
-  // the borders on both sides, 6 * midpoint * ts: the first product is exact in 32 bits, and the fused
-  // multiply-add keeps the difference's sign
-  const float v = e4m3_value(c);
-  if (c < 126) {
-    const float s = fmaf(-3.0f * (v + e4m3_value(c + 1)), ts, amax);
-    if (s > 0.f || (s == 0.f && (c & 1))) return c + 1;
-  }
-  if (c > 0) {
-    const float s = fmaf(-3.0f * (v + e4m3_value(c - 1)), ts, amax);
-    if (s < 0.f || (s == 0.f && (c & 1))) return c - 1;
+  // off by less than 2^-22: where a little less and a little more give one code, it is the right one
+  const float q = amax * __frcp_rn(6.0f * ts);
+  const uint32_t pair = __nv_cvt_float2_to_fp8x2(make_float2(q * (1.0f - 0x1p-21f), q * (1.0f + 0x1p-21f)),
+                                                 __NV_SATFINITE, __NV_E4M3);
+  uint32_t c = pair & 0x7Fu;
+  const uint32_t up = pair >> 8 & 0x7Fu;
+  if (c != up) {
+    // the border between them, 6 * midpoint * ts: the first product is exact in 32 bits, and the fused
+    // multiply-add keeps the difference's sign
+    const float s = fmaf(-3.0f * (e4m3_value(c) + e4m3_value(up)), ts, amax);
+    if (s > 0.f || (s == 0.f && (c & 1u))) c = up;
   }
   return c;
 }
@@ -231,7 +227,7 @@ __global__ void __launch_bounds__(256)
       }
       if ((run & 1) == 0) scales[row * scale_stride + run / 2] = static_cast<uint8_t>(code);
     } else {
-      const int code = finite ? e4m3_scale(amax, ts) : 0x7F;
+      const uint32_t code = finite ? e4m3_scale(amax, ts) : 0x7Fu;
       const float d = finite ? e4m3_value(code) * ts : 0.f;
       const uint32_t db = __float_as_uint(d);
       if (db >= 0x00800000u && db < 0x7F800000u) {  // a unit below the normal range counts as 0
@@ -318,7 +314,7 @@ __global__ void __launch_bounds__(256)
     float d;
     if constexpr (kNv) {
       // the sign bit of a scale is not used by the format
-      d = (s & 0x7Fu) == 0x7Fu ? __int_as_float(0x7fc00000) : e4m3_value(static_cast<int>(s & 0x7Fu)) * ts;
+      d = (s & 0x7Fu) == 0x7Fu ? __int_as_float(0x7fc00000) : e4m3_value(s & 0x7Fu) * ts;
     } else {
       d = s == 0xFFu ? __int_as_float(0x7fc00000) : __uint_as_float(s == 0u ? 1u << 22 : s << 23);
     }

@@ -25,11 +25,12 @@
 //     MMAs that already read 107 of 128 bytes a cycle: turning a stage took 1000 to 3000 cycles
 //     where its MMAs take 768.
 //
-// Measured (B200, NVFP4, 1.9 GHz). 8192 x 4608 x 5120: 103 us, 3.7 PFLOP/s; a stage of 256 x 192 takes
-// 1075 cycles of 768 of MMAs (940 without the TMA's writes: shared memory's bandwidth), a tile's epilogue
-// 2500 that the next tile does not cover. 384 experts of 5120 x 2304, 192 rows, MXFP4: 153 us, 6.1 TB/s of
-// HBM. One row, 4608 x 5120: 8.1 us, of which 6.4 in the kernel: latencies of its first loads, seven stages,
-// two cluster barriers.
+// Measured (B200). NVFP4, 8192 x 4608 x 5120: 102 us with the scales' arrangement, 3.8 PFLOP/s, 4.1 where
+// the tiles fill whole rounds (7872 rows), at the 1000 W cap (1.66 GHz); a stage of 256 x 192 takes 1075
+// cycles of 768 of MMAs (940 without the TMA's writes: shared memory's bandwidth), a tile's epilogue 2500
+// that the next tile does not cover. MXFP4, 384 experts of 5120 x 2304, 192 rows: 153 us, 6.1 TB/s of HBM;
+// 64 experts of 2304 x 5120, 12288 rows: 125 us, of which 10 arrange 24 MB of scales. MXFP4, one row, 4608 x
+// 5120: 8.1 us, of which 6.4 in the kernel: latencies of its first loads, seven stages, two cluster barriers.
 //
 // Few tokens and few tiles: a cluster of `splits` CTAs takes one tile, each a slice of K;
 // the partial tiles meet in the first CTA's shared memory and are summed in slice order.
