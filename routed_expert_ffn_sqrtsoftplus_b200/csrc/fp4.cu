@@ -176,8 +176,8 @@ __device__ __forceinline__ uint32_t settle(uint32_t lo, uint32_t hi, const T* p,
 }
 
 // Runs a thread takes, a block's width apart and loaded together: two of 16-bit values to MXFP4, which
-// HBM bounds (8192 x 5120: 18.3 us against 21.9 with one); one to NVFP4, whose arithmetic bounds it (26
-// us either way), and of 32-bit values, for their registers.
+// HBM bounds (8192 x 5120: 18.3 us against 21.9 with one); one to NVFP4, whose arithmetic bounds it (23.1
+// us against 22.5 with two, but 517 x 1312 2.0 against 2.2), and of 32-bit values, for their registers.
 template <typename T, bool kNv>
 constexpr int kRuns = sizeof(T) == 4 || kNv ? 1 : 2;
 
