@@ -580,7 +580,8 @@ MOE_API moe_status moe_fp4_matmul(const moe_fp4_product* p, moe_stream_t stream)
  * The same with x [T, K] in x_dtype (moe_value_dtype), rows x_row_stride elements apart, quantised
  * first (moe_quantize_fp4 with x_tensor_scale): p->x is x, p->x_scales and p->x_scale_stride are
  * not used, and the workspace has moe_fp4_linear_workspace_bytes(...) bytes (never 0 for T > 0, but
- * for shapes that are refused). T * K <= 2^33 here.
+ * for shapes that are refused), which also has room for aligned rows of w's scales where their count
+ * is no multiple of 8 (MXFP4) or 16 (NVFP4): w_scales may be any there. T * K <= 2^33 here.
  */
 MOE_API int64_t moe_fp4_linear_workspace_bytes(int32_t format, int32_t T, int32_t N, int32_t K, int32_t E);
 MOE_API moe_status moe_fp4_linear(const moe_fp4_product* p, int32_t x_dtype, int64_t x_row_stride,

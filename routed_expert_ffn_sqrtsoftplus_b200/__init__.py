@@ -521,7 +521,9 @@ def fp4_linear(x: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor, fmt: st
     if status is not None:
         _arg(status, "status", torch.int32, (1,), x)
     wss = w_scales.shape[-1]
-    if _fp4_workspace_bytes(False, x.device.index, f, T, N, K, E) == 0:   # the scales are read as they are
+    # scales that are read as they are; rows that no base aligns the call itself copies
+    if w_scales.data_ptr() % 16 != 0 and wss % (16 if f else 8) == 0 and (
+            _fp4_workspace_bytes(False, x.device.index, f, T, N, K, E) == 0):
         w_scales, wss = _aligned_scales(w_scales, f)
     nbytes = _fp4_workspace_bytes(True, x.device.index, f, T, N, K, E)
     space = _bytes(x, nbytes)

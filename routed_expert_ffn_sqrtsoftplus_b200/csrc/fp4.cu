@@ -333,13 +333,13 @@ __global__ void __launch_bounds__(256)
 
 // Scale rows into rows of another stride, 4 bytes of the destination per thread.
 __global__ void __launch_bounds__(256)
-    pad_scales_kernel(const uint8_t* __restrict__ src, int64_t words, int words_per_row, int cols,
+    pad_scales_kernel(const uint8_t* __restrict__ src, int64_t src_stride, int64_t words, int words_per_row, int cols,
                       uint32_t* __restrict__ dst) {
   const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
   if (i >= words) return;
   const int64_t row = i / words_per_row;
   const int c = static_cast<int>(i - row * words_per_row) * 4;
-  const uint8_t* p = src + row * cols + c;
+  const uint8_t* p = src + row * src_stride + c;
   uint32_t w = 0u;
 #pragma unroll
   for (int b = 0; b < 4; ++b)
@@ -387,12 +387,12 @@ cudaError_t launch_quantize_fp4(int format, const void* src, int dtype, int64_t 
   return cudaErrorInvalidValue;
 }
 
-cudaError_t launch_pad_scales(const uint8_t* src, int64_t rows, int cols, uint8_t* dst, int64_t dst_stride,
-                              cudaStream_t s) {
+cudaError_t launch_pad_scales(const uint8_t* src, int64_t src_stride, int64_t rows, int cols, uint8_t* dst,
+                              int64_t dst_stride, cudaStream_t s) {
   if (rows == 0) return cudaSuccess;
   const int wpr = static_cast<int>(dst_stride / 4);
   const int64_t words = rows * wpr;
-  pad_scales_kernel<<<static_cast<unsigned>((words + 255) / 256), 256, 0, s>>>(src, words, wpr, cols,
+  pad_scales_kernel<<<static_cast<unsigned>((words + 255) / 256), 256, 0, s>>>(src, src_stride, words, wpr, cols,
                                                                               reinterpret_cast<uint32_t*>(dst));
   return cudaGetLastError();
 }

@@ -347,9 +347,10 @@ cudaError_t launch_quantize_fp4(int format, const void* src, int dtype, int64_t 
 cudaError_t launch_dequantize_fp4(int format, const uint8_t* codes, const uint8_t* scales, int64_t rows, int cols,
                                   int64_t scale_stride, const float* tensor_scale, void* dst, int dtype,
                                   cudaStream_t s);
-// Scale rows [rows, cols] into rows dst_stride bytes apart (a multiple of 4, at least cols), zeros behind.
-cudaError_t launch_pad_scales(const uint8_t* src, int64_t rows, int cols, uint8_t* dst, int64_t dst_stride,
-                              cudaStream_t s);
+// Scale rows [rows, cols], src_stride bytes apart, into rows dst_stride bytes apart (a multiple of 4, at least
+// cols), zeros behind.
+cudaError_t launch_pad_scales(const uint8_t* src, int64_t src_stride, int64_t rows, int cols, uint8_t* dst,
+                              int64_t dst_stride, cudaStream_t s);
 // y[t, n] = alpha sum_k x[t, k] w[g(t), n, k]; see gemm_fp4.cu
 struct Fp4GemmArgs {
   const uint8_t* xs;            // scales of x, rows xs_stride bytes apart
@@ -375,7 +376,7 @@ struct Fp4Plan {
   int splits;
 };
 Fp4Plan fp4_plan(int T, int N, int E, int num_kb, int num_sms);
-// Scratch that the plan needs (16-byte aligned), or 0.
+// Scratch that the plan's kernels need (16-byte aligned), or 0.
 int64_t fp4_workspace(int format, int T, int N, int E, int num_kb, const Fp4Plan& p);
 cudaError_t launch_gemm_fp4(int format, const CUtensorMap& tm_w, const CUtensorMap& tm_x, Fp4GemmArgs a,
                             void* workspace, const Fp4Plan& p, int num_sms, cudaStream_t s);

@@ -103,6 +103,11 @@ bool scales_ok(const moe_fp4_product& p, const Planned& planned) {
                                p.x_scale_stride % unit == 0 && aligned(p.x_scales, unit));
 }
 
+// Bytes of w's scales in rows that a product without a workspace can read.
+int64_t padded_w(int32_t format, int32_t N, int32_t K, int32_t E) {
+  return padded_scales(format, K) * N * E;
+}
+
 // The launches of a checked product.
 moe_status run_product(const moe_fp4_product& p, const Fp4Plan& plan, cudaStream_t stream) {
   int dev = 0, sms = 0;
@@ -241,7 +246,7 @@ moe_status moe_fp4_pad_scales(const uint8_t* src, int64_t rows, int32_t cols, ui
   if (src == nullptr || dst == nullptr || !aligned(dst, 16)) return MOE_ERR_INVALID_ARG;
   const moe_status st = on_device({src, dst});
   if (st != MOE_OK) return st;
-  return launched(launch_pad_scales(src, rows, cols, dst, dst_stride, as_stream(stream)));
+  return launched(launch_pad_scales(src, cols, rows, cols, dst, dst_stride, as_stream(stream)));
 }
 
 int64_t moe_fp4_workspace_bytes(int32_t format, int32_t T, int32_t N, int32_t K, int32_t E) {
@@ -268,7 +273,9 @@ moe_status moe_fp4_matmul(const moe_fp4_product* p, moe_stream_t stream) {
 int64_t moe_fp4_linear_workspace_bytes(int32_t format, int32_t T, int32_t N, int32_t K, int32_t E) {
   if (!fp4_format_ok(format) || !product_shape_ok(T, N, K, E) || K % 32 != 0 || T == 0 || T > kMaxQuantized / K)
     return 0;
-  return T * (K / 2 + padded_scales(format, K)) + moe_fp4_workspace_bytes(format, T, N, K, E);
+  int64_t bytes = plan_product(format, T, N, K, E).bytes;
+  if (bytes == 0 && K / (format == MOE_FP4_NV ? 16 : 32) % scale_unit(format) != 0) bytes = padded_w(format, N, K, E);
+  return T * (K / 2 + padded_scales(format, K)) + bytes;
 }
 
 moe_status moe_fp4_linear(const moe_fp4_product* p, int32_t x_dtype, int64_t x_row_stride, moe_stream_t stream) {
@@ -292,10 +299,19 @@ moe_status moe_fp4_linear(const moe_fp4_product* p, int32_t x_dtype, int64_t x_r
   q.x_scales = scales;
   q.workspace = codes + own;
   q.workspace_bytes = p->workspace_bytes - own;
-  if (!scales_ok(q, planned)) return MOE_ERR_INVALID_ARG;
+  const bool pad_w = !scales_ok(q, planned);
+  if (pad_w && q.workspace_bytes < padded_w(p->format, p->N, p->K, p->E)) return MOE_ERR_INVALID_ARG;
   st = on_device({p->x, p->w, p->w_scales, p->y, p->offsets, p->x_tensor_scale, p->w_tensor_scale, p->status,
                   p->workspace});
   if (st != MOE_OK) return st;
+  if (pad_w) {  // in front of the quantiser, whose end the product's start then overlaps
+    st = launched(launch_pad_scales(p->w_scales, p->w_scale_stride, static_cast<int64_t>(p->E) * p->N,
+                                    p->K / (p->format == MOE_FP4_NV ? 16 : 32), codes + own, xs_stride,
+                                    as_stream(stream)));
+    if (st != MOE_OK) return st;
+    q.w_scales = codes + own;
+    q.w_scale_stride = xs_stride;
+  }
   st = launched(launch_quantize_fp4(p->format, p->x, x_dtype, p->T, p->K, x_row_stride, p->x_tensor_scale, codes, scales,
                                     q.x_scale_stride, as_stream(stream)));
   if (st != MOE_OK) return st;

@@ -260,6 +260,23 @@ def test_matmul_nan_stays_in_its_row(fmt):
     assert bad.nonzero().flatten().tolist() == [7, 33] and not bool(torch.isnan(y[~bad]).any())
 
 
+@pytest.mark.parametrize("fmt", FMT)
+@pytest.mark.parametrize("K", [96, 288, 512])
+@pytest.mark.parametrize("T", [5, 300])
+def test_weight_scales_at_any_address(fmt, K, T):
+    w, ws, wts = _weights(3, 136, K, fmt, 31)
+    x = _x(T, K, "bf16", 32).cuda()
+    off = torch.tensor([0, 2, 2, T], dtype=torch.int32).cuda()
+    y0 = moe.fp4_linear(x, w, ws, fmt, offsets=off, w_tensor_scale=wts)
+    for at in (1, 8):
+        buf = torch.empty(ws.numel() + at, dtype=torch.uint8, device="cuda")
+        moved = buf[at:].view(ws.shape)
+        moved.copy_(ws)
+        assert torch.equal(y0, moe.fp4_linear(x, w, moved, fmt, offsets=off, w_tensor_scale=wts))
+        c, s = moe.quantize_fp4(x, fmt)
+        assert torch.equal(y0, moe.fp4_matmul(c, s, w, moved, fmt, offsets=off, w_tensor_scale=wts))
+
+
 def test_strided_x_streams_and_graphs():
     x = torch.randn((300, 416), generator=_gen(4)).to(torch.bfloat16).cuda()
     w, ws, wts = _weights(1, 256, 384, "nvfp4", 5)

@@ -102,7 +102,7 @@ def test_fp4_matmul_refuses_bad_arguments(L, kw, want):
     if not any(n.startswith("x_scale") for n in kw) and "workspace" not in kw and kw.get("format") != 1:
         # the same with x to be quantised: x's scales are not given, and there is always a workspace
         big = dict(dict(workspace=FAKE, workspace_bytes=1 << 40), **kw)
-        if kw.get("x", 0) != FAKE + 4 and kw.get("T") != 4096:
+        if kw.get("x", 0) != FAKE + 4 and kw.get("T") != 4096 and kw.get("w_scale_stride") != 12:   # copied there
             assert L.moe_fp4_linear(_product(**big), 2, 1 << 20, None) == want
     assert L.moe_fp4_matmul(None, None) == INV
     w = L.moe_fp4_workspace_bytes
@@ -112,10 +112,13 @@ def test_fp4_matmul_refuses_bad_arguments(L, kw, want):
 
 def test_fp4_linear_refuses_bad_arguments(L):
     w = L.moe_fp4_linear_workspace_bytes
-    assert w(0, 4, 64, 64, 1) == 4 * (32 + 16) and w(0, 4, 64, 48, 1) == 0 and w(0, 0, 64, 64, 1) == 0
+    assert w(0, 4, 64, 256, 1) == 4 * (128 + 16) and w(0, 4, 64, 48, 1) == 0 and w(0, 0, 64, 64, 1) == 0
+    assert w(0, 4, 64, 64, 1) == 4 * (32 + 16) + 64 * 16      # aligned rows of w's scales
+    assert w(1, 4, 64, 288, 2) == 4 * (144 + 32) + 128 * 32
     f = lambda dt=0, rs=64, **kw: L.moe_fp4_linear(_product(**dict(dict(workspace=FAKE, workspace_bytes=1 << 20), **kw)), dt, rs, None)  # noqa: E731
     assert f(dt=3) == INV and f(rs=63) == INV and f(x=FAKE + 1) == INV and f(x=None) == INV
     assert f(workspace=None) == INV and f(workspace_bytes=4 * 48 - 1) == INV and f(workspace=FAKE + 8) == INV
+    assert f(w_scale_stride=12, workspace_bytes=4 * 48 + 64 * 16 - 1) == INV
     assert L.moe_fp4_linear(None, 0, 64, None) == INV and f(T=0) == OK
     # the quantiser counts in 32 bits: 2^33 values a call
     assert f(T=1 << 20, K=1 << 14, w_scale_stride=1 << 10, rs=1 << 14) == UNS
