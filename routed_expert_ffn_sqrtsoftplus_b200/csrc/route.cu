@@ -15,7 +15,7 @@
 //
 // Exactness. Without a bias the three scores grow with the logit, so the logits
 // themselves are the keys and the selection is exact. With a bias, or where a group is
-// worth the sum of two scores, keys are 32-bit sums with a small error (key_tol). Where
+// worth the sum of two scores, keys are 32-bit sums with a small error (kKeyTol). Where
 // two neighbours of a row's selection are nearer than that, the experts that may belong
 // to it, one per lane, are put in order by 64-bit keys (order_f64); where it is the groups
 // that cannot be told apart, the experts that may count in their worth are (groups_f64). A row
@@ -37,12 +37,17 @@ namespace {
 constexpr int kRouteWarps = 4;  // rows per block
 constexpr uint32_t kFull = 0xffffffffu;
 
-// Two 32-bit keys may stand in the wrong order where they are no further apart than this, times 1 + |key|.
-// Sigmoid: __expf is off by 2 + 1.2 |x| units of 2^-23, of which u / (1 + u)^2 (at most 0.6 units in all)
-// reaches the score; the quotient, 1 + u and the sum with the bias add two: below 2^-21 a key. The terms of
-// sqrt(log(1 + e^z)) are good to a unit each. Softmax: the sum of up to 512 terms adds up to 21 roundings.
-__device__ __forceinline__ float key_tol(int score) {
-  return score == kScoreSoftmax ? 3.814697265625e-6f : 9.5367431640625e-7f;  // 2^-18, 2^-20
+// Two 32-bit keys may stand in the wrong order where they are no further apart than this, times key_base + |key|: the
+// sum with the bias rounds with the key (half a unit of 2^-23 each), the scores' own errors do not shrink with what a
+// bias leaves of them.
+constexpr float kKeyTol = 2.384185791015625e-7f;  // 2^-22
+// The error of two scores, in that unit. Sigmoid: __expf is off by 2 + 1.2 |x| units of 2^-23, of which u / (1 + u)^2
+// (at most 0.6 units in all) reaches the score; the quotient and 1 + u add two at most. Softmax: the sum of up to
+// 512 terms adds up to 21 roundings. sqrt(log(1 + e^z)) is not bounded: e^z is good to two units of 2^-23 of itself, its
+// logarithm to one more, the sum with z to half of one; the root halves that and adds half a unit: at most 2.25 units of
+// the score, which is sqrt(zmax + 0.7) at most.
+__device__ __forceinline__ float key_base(int score, float zmax) {
+  return score == kScoreSoftmax ? 16.0f : score == kScoreSigmoid ? 4.0f : 2.5f * sqrtf(fmaxf(zmax, 0.0f) + 0.7f);
 }
 
 template <typename T>
@@ -349,7 +354,7 @@ __device__ __forceinline__ int select_by_rounds(uint32_t (&key)[EPL], int e0, in
 
 // By a list: the k-th largest of the lanes' maxima (with 12 keys a lane or more, of their halves' maxima)
 // bounds the k-th largest key from below, and few keys reach that bound. They go to a list of at most 32 (key, expert), one a lane, and each counts those ahead of
-// it. -1 where there are more; `tol` lowers the bound, so that the list also holds what
+// it. -1 where there are more; `base` (key_base, or 0 for keys that are exact) lowers the bound, so that the list also holds what
 // floats cannot tell from the last slot. Some 200 instructions where rounds take 60 each.
 //
 // Halves where they are long: of 512 experts in 8 groups, 4 of them kept, 16 lanes are live, and a list for 16
@@ -357,7 +362,7 @@ __device__ __forceinline__ int select_by_rounds(uint32_t (&key)[EPL], int e0, in
 // without groups, 12 slots, 26.5 against 25.6). Above 16 slots the bound lets too many through either way.
 constexpr int kListK = 16;
 template <int EPL>
-__device__ __forceinline__ int select_by_list(const uint32_t (&key)[EPL], int e0, int k, float tol, uint2* list,
+__device__ __forceinline__ int select_by_list(const uint32_t (&key)[EPL], int e0, int k, float base, uint2* list,
                                               int lane, int& mine, uint32_t& mkey, uint32_t& left) {
   constexpr int kParts = EPL >= 12 ? 2 : 1, kLen = EPL / kParts;
   uint32_t bk[kParts];
@@ -388,9 +393,9 @@ __device__ __forceinline__ int select_by_list(const uint32_t (&key)[EPL], int e0
   }
   // fewer than k parts with live experts: everything live
   if (reached < k || bound == 0u) bound = 1u;
-  if (tol > 0.f && bound > 1u) {
+  if (base > 0.f && bound > 1u) {
     const float f = value_of(bound);
-    bound = max(1u, key_of(f - tol * (1.0f + fabsf(f))));
+    bound = max(1u, key_of(f - kKeyTol * (base + fabsf(f))));
   }
   int n = 0;
 #pragma unroll
@@ -422,8 +427,10 @@ __device__ __forceinline__ int select_by_list(const uint32_t (&key)[EPL], int e0
   return min(n, k);
 }
 
+// The second bound keeps the widest rows at the registers of 5 and 6 blocks an SM (16384 x 512, 12 BF16 slots 26.4 us;
+// 31.7 with the 108 registers that the compiler takes without it).
 template <typename T, int EPL>
-__global__ void __launch_bounds__(kRouteWarps * 32)
+__global__ void __launch_bounds__(kRouteWarps * 32, EPL < 16 ? 1 : sizeof(T) == 4 ? 5 : 6)
     route_kernel(const T* __restrict__ logits, int64_t row_stride, const float* __restrict__ bias, int rows,
                  SelectArgs a, int renorm, float scale, int vec, int vec_bias, int32_t* __restrict__ idx_out,
                  float* __restrict__ w_out) {
@@ -446,8 +453,9 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
   }
   const bool grouped = a.kept < a.G;
   const bool need_scores = bias != nullptr || (grouped && a.sum2);
-  const float tol = key_tol(a.score);
   float inv_sum = 1.0f;
+  float base = 0.0f;
+  if (need_scores) base = key_base(a.score, value_of(__reduce_max_sync(kFull, key_of(zmax))));
   if (a.score == kScoreSoftmax) {
     zmax = warp_max(zmax);
     if (need_scores || !renorm) {
@@ -528,7 +536,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
     // no more than err
     const bool two = a.sum2 && w2 != -INFINITY;
     float worth = a.sum2 ? 0.5f * w1 + 0.5f * (two ? w2 : 0.f) : w1;
-    const float err = 0.5f * tol * (1.0f + (two ? 0.5f * fabsf(w1) + 0.5f * fabsf(w2) : fabsf(w1)));
+    const float err = 0.5f * kKeyTol * (base + (two ? 0.5f * fabsf(w1) + 0.5f * fabsf(w2) : fabsf(w1)));
     if (lane >= a.G) worth = -INFINITY;
     int rank = 0;
 #pragma unroll 4
@@ -545,7 +553,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
       if (least <= most) {
         // of each group, what reaches its second (or its first) key
         const float low = a.sum2 && w2 != -INFINITY ? w2 : w1;
-        const float from = lane < a.G ? low - tol * (1.0f + fabsf(low)) : INFINITY;
+        const float from = lane < a.G ? low - kKeyTol * (base + fabsf(low)) : INFINITY;
         Gather cands;
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
@@ -585,17 +593,17 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
   int mine = -1, n = 0;  // slot `lane`'s expert; slots filled
   uint32_t mkey = 0u, left = 0u;  // its key, and the best one left
   if (a.k <= kListK)
-    n = select_by_list<EPL>(key, e0, a.k, bias != nullptr ? tol : 0.f, list_buf[warp], lane, mine, mkey, left);
+    n = select_by_list<EPL>(key, e0, a.k, bias != nullptr ? base : 0.f, list_buf[warp], lane, mine, mkey, left);
   if (a.k > kListK || n < 0) n = select_by_rounds<EPL>(key, e0, a.k, lane, mine, mkey, left);
   if (bias != nullptr) {
     // neighbours that 32-bit keys do not tell apart: order what reaches down to the last slot's key again
     uint32_t next = __shfl_down_sync(kFull, mkey, 1);
     if (lane == n - 1) next = left;
     const float mine_f = value_of(mkey);
-    const bool close = lane < n && next != 0u && mine_f - value_of(next) <= tol * (1.0f + fabsf(mine_f));
+    const bool close = lane < n && next != 0u && mine_f - value_of(next) <= kKeyTol * (base + fabsf(mine_f));
     if (!unsure && __any_sync(kFull, close)) {
       const float last = __shfl_sync(kFull, mine_f, n - 1);
-      const float least = last - tol * (1.0f + fabsf(last));
+      const float least = last - kKeyTol * (base + fabsf(last));
       Gather cands;
 #pragma unroll
       for (int i = 0; i < EPL; ++i)  // with a bias v holds the keys, -infinity where the expert is out

@@ -358,3 +358,40 @@ def test_forward_routed_bad_indices(tiny):
         layer.forward_routed(x, idx[:, :3].contiguous(), w)
     with pytest.raises(ValueError):
         layer.forward_routed(x, idx.long(), w)
+
+
+def _cancelling_rows(level, T, E, seed):
+    """Logits about `level` whose sqrtsoftplus scores a bias takes back to keys of some 1e-5."""
+    g = torch.Generator().manual_seed(seed)
+    z0 = level * (0.8 + 0.4 * torch.rand(E, generator=g).double())
+    bias = (-torch.sqrt(torch.nn.functional.softplus(z0))).float()
+    want = -bias.double() + 1e-5 * torch.randn((T, E), generator=g).double()   # the score: key + |bias|
+    return torch.log(torch.expm1(want ** 2)).where(want ** 2 < 30, want ** 2).float(), bias
+
+
+@pytest.mark.parametrize("level", [1.0, 300.0, 1500.0, 1e4])
+@pytest.mark.parametrize("E,k", [(8, 2), (16, 3), (64, 1), (64, 8), (200, 12), (512, 32)])
+def test_route_sqrtsoftplus_scores_that_a_bias_cancels(level, E, k):
+    """A score's 32-bit error goes with the score, not with the small key that the bias leaves of it."""
+    z, bias = _cancelling_rows(level, 60 if E > 16 else 400, E, E + k)
+    z[1::3] += 0.5 * torch.randn(z[1::3].shape, generator=torch.Generator().manual_seed(k))  # next to ordinary rows
+    for G, kept, group in ((1, 1, "max"), (4, 2, "top2"), (4, 2, "max")):
+        _check(z.cuda(), k, "sqrtsoftplus", bias.cuda(), G, kept, group)
+
+
+def test_route_cancelled_scores_by_hand():
+    # sqrt(1501.1384) - 38.744522 = 5.6187e-6 against 5.5007e-6, in 32 bits 3.8e-6 against 5.7e-6;
+    # sqrt(1036.16) - 32.18944 = -1.888e-6 against -1.875e-6, in 32 bits 0 against -1.85e-6
+    for z, b, first in (([1501.1384, 160.7942], [-38.744522, -12.680460], 0), ([1036.16, 0.0], [-32.18944, -0.8325565], 1)):
+        idx, _ = _check(torch.tensor([z]).cuda(), 1, "sqrtsoftplus", torch.tensor(b).cuda())
+        assert idx.item() == first
+
+
+@pytest.mark.parametrize("k", [9, 12, 16, 17, 32])
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid", "sqrtsoftplus"])
+def test_route_many_slots_groups_and_bias(kind, k):
+    g = torch.Generator().manual_seed(k)
+    for E, G, kept in ((512, 8, 4), (512, 8, 1), (480, 5, 2), (256, 32, 9)):
+        bias = (torch.randn(E, generator=g) * 0.1).cuda()
+        for dtype in ("fp32", "bf16"):
+            _check(_logits(33, E, dtype, E + k, off=5), k, kind, bias, G, kept)
