@@ -134,15 +134,18 @@ __device__ __forceinline__ float sigmoid_f32(float z) {
 __device__ __forceinline__ float score_f32(float z, int score, float m, float inv_sum) {
   if (score == kScoreSoftmax) return expf(z - m) * inv_sum;
   if (score == kScoreSigmoid) return sigmoid_f32(z);
+  // far down log(1 + e^z) is e^z (to e^z / 2 of itself), whose root is an ordinary number where e^z is none
+  if (z < -20.0f) return expf(0.5f * z);
   return sqrtf(fmaxf(z, 0.0f) + log1pf(expf(-fabsf(z))));
 }
-// The same for keys.
+// The same for keys, whose error is an absolute one.
 __device__ __forceinline__ float key_score(float z, int score, float m, float inv_sum) {
   if (score == kScoreSigmoid) {
     const float u = __expf(-fabsf(z));
     return __fdividef(z >= 0.0f ? 1.0f : u, 1.0f + u);
   }
-  return score_f32(z, score, m, inv_sum);
+  if (score == kScoreSoftmax) return expf(z - m) * inv_sum;
+  return sqrtf(fmaxf(z, 0.0f) + log1pf(expf(-fabsf(z))));
 }
 __device__ __forceinline__ double score_f64(double z, int score, double m, double sum) {
   if (score == kScoreSoftmax) return exp(z - m) / sum;

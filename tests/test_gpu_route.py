@@ -395,3 +395,21 @@ def test_route_many_slots_groups_and_bias(kind, k):
         bias = (torch.randn(E, generator=g) * 0.1).cuda()
         for dtype in ("fp32", "bf16"):
             _check(_logits(33, E, dtype, E + k, off=5), k, kind, bias, G, kept)
+
+
+@pytest.mark.parametrize("kind", ["sigmoid", "sqrtsoftplus"])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_route_low_logits_without_renormalisation(kind, dtype):
+    """Scores that are ordinary 32-bit numbers although e^z is not: sqrt(log(1 + e^z)) is e^-80 at z = -160."""
+    z = -torch.linspace(15.0, 80.0 if kind == "sigmoid" else 160.0, 60).repeat(3, 1)
+    z[1] = z[1].flip(0)
+    z[2, 1::2] = -float("inf")
+    z = z.to(DT[dtype]).cuda()
+    _check(z, 12, kind, renorm=False, scale=1.5)
+    far = z[:, -12:]                 # the lowest ones, as the only experts of their rows
+    idx, w = _check(far, 12, kind, renorm=False, scale=1.5)
+    g = torch.randn((3, 12), generator=torch.Generator().manual_seed(3)).cuda()
+    got = moe.route_backward(g, far, idx, score=kind, renormalize=False, route_scale=1.5).double().cpu().numpy()
+    want = _grad_ref(far.double().cpu().numpy(), idx.cpu().numpy(), g.double().cpu().numpy(), kind, False, 1.5)
+    # one term an element: the bound is relative to itself
+    assert (np.abs(got - want) <= (64 * 2.0 ** -24 + torch.finfo(DT[dtype]).eps / 2) * np.abs(want)).all()
