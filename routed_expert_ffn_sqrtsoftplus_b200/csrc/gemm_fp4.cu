@@ -148,12 +148,12 @@ __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // Store to the same shared-memory address of another CTA of the cluster.
-__device__ __forceinline__ void st_cluster_f32(uint32_t saddr, uint32_t rank, float v) {
+__device__ __forceinline__ void st_cluster_u32(uint32_t saddr, uint32_t rank, uint32_t v) {
   asm volatile(
       "{\n\t.reg .b32 a;\n\t"
       "mapa.shared::cluster.u32 a, %0, %1;\n\t"
-      "st.shared::cluster.f32 [a], %2;\n\t}\n" ::"r"(saddr),
-      "r"(rank), "f"(v)
+      "st.shared::cluster.u32 [a], %2;\n\t}\n" ::"r"(saddr),
+      "r"(rank), "r"(v)
       : "memory");
 }
 
@@ -809,12 +809,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (rank != 0) {
         const uint32_t dst = smem_u32(sA) + (((rank - 1) * kBN + cfirst) * 128 + q * 32 + lane) * 4;
 #pragma unroll
-        for (int j = 0; j < 16; ++j) st_cluster_f32(dst + j * 512, 0, __uint_as_float(r[j]));
+        for (int j = 0; j < 16; ++j) st_cluster_u32(dst + j * 512, 0, r[j]);
       }
     }
+    // a CTA that gave up has no part to add: the first one then writes nothing
+    if (threadIdx.x == 0 && rank != 0 && *abort_flag) st_cluster_u32(smem_u32(const_cast<int*>(abort_flag)), 0, 1u);
     __syncwarp();
     cluster_sync_all();
-    if (work && rank == 0 && cfirst < tl.rows) {
+    if (work && rank == 0 && !*abort_flag && cfirst < tl.rows) {
       const float* part = reinterpret_cast<const float*>(sA) + cfirst * 128 + q * 32 + lane;
       for (int p = 0; p < splits - 1; ++p)
 #pragma unroll
