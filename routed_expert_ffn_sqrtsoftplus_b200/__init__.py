@@ -39,7 +39,7 @@ EXPORTED = ("moe_create", "moe_forward", "moe_forward_host", "moe_get_status", "
             "moe_forward_partial", "moe_read_bandwidth", "moe_forward_host_async", "moe_forward_host_wait",
             "moe_route", "moe_route_backward", "moe_forward_routed", "moe_quantize_fp4", "moe_dequantize_fp4",
             "moe_fp4_pad_scales", "moe_fp4_workspace_bytes", "moe_fp4_matmul",
-            "moe_fp4_linear_workspace_bytes", "moe_fp4_linear")
+            "moe_fp4_linear_workspace_bytes", "moe_fp4_linear", "moe_fp4_set_wait_timeout")
 
 SCORES = {"softmax": 0, "sigmoid": 1, "sqrtsoftplus": 2}
 FP4_FORMATS = {"mxfp4": 0, "nvfp4": 1}
@@ -135,6 +135,7 @@ def lib() -> ctypes.CDLL:
             "moe_fp4_matmul": (I32, [ctypes.POINTER(_Fp4Product), P]),
             "moe_fp4_linear_workspace_bytes": (I64, [I32, I32, I32, I32, I32]),
             "moe_fp4_linear": (I32, [ctypes.POINTER(_Fp4Product), I32, I64, P]),
+            "moe_fp4_set_wait_timeout": (I32, [U64]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -451,6 +452,13 @@ def _fp4_workspace_bytes(linear, device, *shape):
         raise ValueError("an FP4 product takes fewer than 2^31 rows, columns and experts")
     L = lib()
     return (L.moe_fp4_linear_workspace_bytes if linear else L.moe_fp4_workspace_bytes)(*shape)
+
+
+def fp4_set_wait_timeout(ns: int):
+    """Limit of the device-side waits of the FP4 products from now on (the process's; default 2 s)."""
+    if not 1 <= ns < 1 << 64:
+        raise ValueError(f"the limit must be 1 .. 2^64 - 1 ns, got {ns}")
+    _check(lib().moe_fp4_set_wait_timeout(ns), "moe_fp4_set_wait_timeout")
 
 
 def fp4_matmul(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor, fmt: str, *,

@@ -36,7 +36,8 @@
 // the partial tiles meet in the first CTA's shared memory and are summed in slice order.
 //
 // Every read of offsets is clamped to [0, T] and to ascending order, so no offsets lead
-// outside x or y. All waits are bounded.
+// outside x or y. All waits are bounded; one that runs out makes its CTA give up, and the elements of y that it had
+// not written yet stay as they were.
 #include <cuda_fp16.h>
 
 #include <atomic>
@@ -57,6 +58,9 @@ constexpr int kRowBytes = kBK / 2;    // 128: one swizzle row
 constexpr int kBox = 32;              // token rows per TMA box
 constexpr int kMaxExperts = 512;
 constexpr int kMaxSplits = 8;
+// Limit of the waits for a CTA's own copies and MMAs at its end, whatever the limit of the others: what is in flight
+// then writes to memory that the CTA gives back.
+constexpr uint64_t kDrainNs = 2000000000ull;
 
 // kHalves: 128-row halves of w per tile; kBN: rows of x per tile.
 template <bool kNv, bool kPre, int kHalves, int kBN>
@@ -88,7 +92,7 @@ struct Cfg {
   static constexpr int kRaw = kPre ? kStages : 6;
   static constexpr int kSmemBytes = kFixed + kRaw * kRawBytes + kStages * (kABytes + kBBytes);
   static_assert(kSfBase + kSets * kSfCols <= 512 && kSets <= kRaw && kStages >= 2, "TMEM, ring");
-  static_assert((2 * kStages + 3 * kRaw + 2 * kAccs + 1) * 8 + 8 <= 512, "barriers");
+  static_assert((2 * kStages + 3 * kRaw + 2 * kAccs + 1) * 8 + 16 <= 512, "barriers");
   // the partial tiles of a split fit in the ring (kHalves == 1, kBN == 32)
   static_assert(kHalves > 1 || kBN > 32 || (kMaxSplits - 1) * 128 * 32 * 4 <= kStages * (kABytes + kBBytes), "split");
 };
@@ -205,6 +209,15 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, unsign
     }
   }
   return true;
+}
+
+// Waits until the last `stages` of a ring's copies issued so far have landed.
+__device__ __noinline__ void drain_ring(uint64_t* full, int stages, long issued) {
+  for (long i = issued - 1; i >= 0 && i >= issued - stages; --i) {
+    const uint64_t b = globaltimer_ns();
+    while (!mbar_try_wait(&full[i % stages], static_cast<uint32_t>((i / stages) & 1)) && globaltimer_ns() - b < kDrainNs) {
+    }
+  }
 }
 
 // A value that is the same in all lanes, into a uniform register.
@@ -394,6 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* drain = rempty + C::kRaw;
   uint32_t* tmem_base_smem = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_base_smem + 1);
+  volatile long* issued_s = reinterpret_cast<volatile long*>(tmem_base_smem + 2);  // stages that the producer issued
   int* pre = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(bars) + 512);  // [E + 1] first token tile
   int* row_s = pre + kMaxExperts + 1;                                         // [E + 1] first row
 
@@ -484,15 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!ok) break;
       }
-      if (*abort_flag) {
-        // let the copies in flight land before the CTA's shared memory goes
-        for (long i = issued - 1; i >= 0 && i >= issued - C::kStages; --i) {
-          const uint64_t b = globaltimer_ns();
-          while (!mbar_try_wait(&full[i % C::kStages], static_cast<uint32_t>((i / C::kStages) & 1)) &&
-                 globaltimer_ns() - b < args.timeout_ns) {
-          }
-        }
-      }
+      *issued_s = issued;
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
@@ -641,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (elected) {
       umma_commit(drain);
       const uint64_t b = globaltimer_ns();
-      while (!mbar_try_wait(drain, 0) && globaltimer_ns() - b < args.timeout_ns) {
+      while (!mbar_try_wait(drain, 0) && globaltimer_ns() - b < kDrainNs) {
       }
     }
     __syncwarp();
@@ -741,8 +747,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (args.out_dtype == kValFp32) {
 #pragma unroll 1
           for (int c0 = cfirst; c0 < tl.rows; c0 += 16 * C::kEpiGroups) {
-#pragma unroll 1
-            for (int h = 0; h < kHalves; ++h) {
+#pragma unroll
+            for (int h = 0; h < kHalves; ++h) {  // (as a loop it cost 142 to 147 us, by its place, instead of 139: 8192 x 4608 x 5120)
               uint32_t r[16];
               tmem_ld16(tb + h * kBN + c0, r);
               tmem_ld_wait();
@@ -837,6 +843,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  // where the CTA gave up, whichever warp did and when: its copies land before its shared memory goes (asked here, as the
+  // producer may be through before another warp gives up)
+  if (threadIdx.x == 0 && *abort_flag) drain_ring(full, C::kStages, *issued_s);
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem_base, 512);

@@ -1,5 +1,6 @@
 // Entry points of the operators that need no handle: routing from logits and its gradient, and
 // the microscaled FP4 quantisers and product. Arguments are checked before anything is enqueued.
+#include <atomic>
 #include <cmath>
 #include <initializer_list>
 
@@ -11,7 +12,7 @@ using namespace moe;
 
 namespace {
 
-constexpr unsigned long long kWaitNs = 2000000000ull;  // limit of every device-side wait
+std::atomic<uint64_t> wait_ns{2000000000ull};  // limit of every device-side wait
 
 cudaStream_t as_stream(moe_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
 
@@ -130,7 +131,7 @@ moe_status run_product(const moe_fp4_product& p, const Fp4Plan& plan, cudaStream
   a.out = p.y;
   a.out_dtype = p.out_dtype;
   a.status = p.status;
-  a.timeout_ns = kWaitNs;
+  a.timeout_ns = wait_ns.load(std::memory_order_relaxed);
   a.splits = plan.splits;
   a.m_tiles = (p.N + plan.cols - 1) / plan.cols;
   CUtensorMap tw, tx;
@@ -268,6 +269,12 @@ moe_status moe_fp4_matmul(const moe_fp4_product* p, moe_stream_t stream) {
                   p->status, p->workspace});
   if (st != MOE_OK) return st;
   return run_product(*p, planned.plan, as_stream(stream));
+}
+
+moe_status moe_fp4_set_wait_timeout(uint64_t timeout_ns) {
+  if (timeout_ns == 0) return MOE_ERR_INVALID_ARG;
+  wait_ns.store(timeout_ns, std::memory_order_relaxed);
+  return MOE_OK;
 }
 
 int64_t moe_fp4_linear_workspace_bytes(int32_t format, int32_t T, int32_t N, int32_t K, int32_t E) {

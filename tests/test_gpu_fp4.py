@@ -427,3 +427,36 @@ def test_route_then_experts():
         want[t] += float(w.flatten()[s]) * (dv @ hv[r])
         mag[t] += float(w.flatten()[s]) * (np.abs(dv) @ np.abs(hv[r]))
     assert (np.abs(y.double().cpu().numpy() - want) <= mag * 16 * 2.0 ** -24).all()
+
+
+@pytest.mark.parametrize("fmt", FMT)
+@pytest.mark.parametrize("E,T,N,K", [(1, 1, 2304, 262144), (160, 160, 256, 65536), (1, 600, 512, 65536)],
+                         ids=["split", "32 tokens", "arranged"])
+def test_waits_that_run_out(fmt, E, T, N, K):
+    """A tile takes longer than a limit of a microsecond: the call ends, says so, and spoils neither y nor the next call.
+
+    Each element is right or as it was; the kernels' waits all have limits, and copies in flight are waited for.
+    """
+    bs = ref.BLOCK[fmt]
+    g = torch.Generator(device="cuda").manual_seed(3)
+    w = torch.randint(0, 256, (E, N, K // 2), generator=g, device="cuda", dtype=torch.uint8)
+    ws = torch.randint(*((118, 124) if fmt == "mxfp4" else (40, 60)), (E, N, K // bs), generator=g, device="cuda", dtype=torch.uint8)
+    x = torch.randn((T, K), generator=g, device="cuda").to(torch.bfloat16)
+    off = torch.arange(E + 1, dtype=torch.int32, device="cuda") if E > 1 else None
+    if E == 1:
+        w, ws = w[0], ws[0]
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    want = moe.fp4_linear(x, w, ws, fmt, offsets=off, status=status)
+    assert status.item() == 0 and bool(torch.isfinite(want).all())
+    try:
+        moe.fp4_set_wait_timeout(1000)
+        for _ in range(3):
+            y = torch.full((T, N), 7.0, dtype=torch.bfloat16, device="cuda")
+            status.zero_()
+            moe.fp4_linear(x, w, ws, fmt, offsets=off, out=y, status=status)
+            assert status.item() == 1
+            assert bool(((y == want) | (y == 7.0)).all())
+    finally:
+        moe.fp4_set_wait_timeout(2_000_000_000)
+    status.zero_()
+    assert torch.equal(want, moe.fp4_linear(x, w, ws, fmt, offsets=off, status=status)) and status.item() == 0

@@ -194,3 +194,10 @@ def test_bindings_refuse_sizes_that_32_bits_do_not_hold(L):
     for shape in ((1 << 31, 8), ((1 << 32) + 3, 1), (1, 1 << 31)):
         with pytest.raises(ValueError):
             moe._rows(Rows(*shape), "x")
+
+
+def test_wait_limit_refusals(L):
+    assert L.moe_fp4_set_wait_timeout(0) == INV and L.moe_fp4_set_wait_timeout(2_000_000_000) == OK
+    for ns in (0, -1, 1 << 64):
+        with pytest.raises(ValueError):
+            moe.fp4_set_wait_timeout(ns)
