@@ -543,8 +543,8 @@ MOE_API moe_status moe_dequantize_fp4(int32_t format, const uint8_t* codes, cons
  *   y [T, N] contiguous, out_dtype (moe_value_dtype), may not be x
  *   workspace: moe_fp4_workspace_bytes(...) bytes, 16-byte aligned (NULL where that is 0); scratch
  *          of this call, free once the stream is through it. Two calls that may overlap need one each
- *   status: int32 device word that a device-side wait which ran out sets to 1, or NULL. y is then not
- *          complete: elements are right or left as they were
+ *   status: int32 device word that a device-side wait which ran out sets to 1, or NULL:
+ *          moe_fp4_get_status() then tells. y is not complete after that: elements are right or left as they were
  * Limits: T <= 2^22, N and K <= 2^18, E <= 512. No allocation, no synchronisation.
  */
 typedef struct {
@@ -580,6 +580,10 @@ MOE_API moe_status moe_fp4_matmul(const moe_fp4_product* p, moe_stream_t stream)
 /* Limit, in nanoseconds, of every device-side wait of the products enqueued (or captured) from now on, by any
  * thread and on any device (default 2e9; 0 is refused). Suspended waits look at it every 20 us. */
 MOE_API moe_status moe_fp4_set_wait_timeout(uint64_t timeout_ns);
+
+/* Synchronise the current device, then report and clear whether a device-side wait ran out in any product on it that
+ * was given no status word (MOE_OK or MOE_ERR_TIMEOUT); MOE_ERR_CUDA if the synchronisation failed. */
+MOE_API moe_status moe_fp4_get_status(void);
 
 /*
  * The same with x [T, K] in x_dtype (moe_value_dtype), rows x_row_stride elements apart, quantised

@@ -39,7 +39,8 @@ EXPORTED = ("moe_create", "moe_forward", "moe_forward_host", "moe_get_status", "
             "moe_forward_partial", "moe_read_bandwidth", "moe_forward_host_async", "moe_forward_host_wait",
             "moe_route", "moe_route_backward", "moe_forward_routed", "moe_quantize_fp4", "moe_dequantize_fp4",
             "moe_fp4_pad_scales", "moe_fp4_workspace_bytes", "moe_fp4_matmul",
-            "moe_fp4_linear_workspace_bytes", "moe_fp4_linear", "moe_fp4_set_wait_timeout")
+            "moe_fp4_linear_workspace_bytes", "moe_fp4_linear", "moe_fp4_set_wait_timeout",
+            "moe_fp4_get_status")
 
 SCORES = {"softmax": 0, "sigmoid": 1, "sqrtsoftplus": 2}
 FP4_FORMATS = {"mxfp4": 0, "nvfp4": 1}
@@ -136,6 +137,7 @@ def lib() -> ctypes.CDLL:
             "moe_fp4_linear_workspace_bytes": (I64, [I32, I32, I32, I32, I32]),
             "moe_fp4_linear": (I32, [ctypes.POINTER(_Fp4Product), I32, I64, P]),
             "moe_fp4_set_wait_timeout": (I32, [U64]),
+            "moe_fp4_get_status": (I32, []),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -461,6 +463,12 @@ def fp4_set_wait_timeout(ns: int):
     _check(lib().moe_fp4_set_wait_timeout(ns), "moe_fp4_set_wait_timeout")
 
 
+def fp4_status() -> int:
+    """Whether a device-side wait ran out in FP4 products on the current device that were given no status word
+    (MOE_OK or MOE_ERR_TIMEOUT); synchronises the device, and clears it."""
+    return lib().moe_fp4_get_status()
+
+
 def fp4_matmul(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor, fmt: str, *,
                x_tensor_scale: Optional[torch.Tensor] = None, w_tensor_scale: Optional[torch.Tensor] = None,
                offsets: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
@@ -470,7 +478,8 @@ def fp4_matmul(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_scale
 
     With offsets (int32 [E + 1], on the device) w is [E, N, K/2] and rows offsets[g] .. offsets[g + 1] of x meet
     w[g]; rows in no range are left as they were in ``out`` (not set where out is None). w_tensor_scale: one value
-    per expert. status: int32 [1], set to 1 if a device-side wait ran out.
+    per expert. status: int32 [1], set to 1 if a device-side wait ran out (without it fp4_status() tells); elements of
+    y are then right or left as they were.
     """
     if stream is not None:
         with _on_stream(stream):

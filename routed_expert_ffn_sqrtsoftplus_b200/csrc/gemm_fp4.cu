@@ -161,6 +161,12 @@ __device__ __forceinline__ void st_cluster_u32(uint32_t saddr, uint32_t rank, ui
       : "memory");
 }
 
+// Where a wait that ran out is recorded when the caller gave no word for it: one per device, for all its calls.
+__device__ int product_status;
+__device__ __forceinline__ void report_timeout(int* status) {
+  report_status(status != nullptr ? status : &product_status, kStatusTimeout);
+}
+
 // mbarrier.try_wait that may suspend the thread for up to 20 us (it wakes when the phase completes).
 __device__ __forceinline__ bool try_wait_suspended(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
@@ -188,7 +194,7 @@ __device__ __noinline__ bool wait_longer(uint64_t* bar, uint32_t parity, unsigne
     if (*abort_flag) return false;
     if (globaltimer_ns() - t0 > timeout_ns) {
       *abort_flag = 1;
-      report_status(status, kStatusTimeout);
+      report_timeout(status);
       return false;
     }
   }
@@ -641,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (!ok && elected) {
       *abort_flag = 1;
-      report_status(args.status, kStatusTimeout);
+      report_timeout(args.status);
     }
     // every MMA done before TMEM and shared memory go
     if (elected) {
@@ -1091,6 +1097,14 @@ Fp4Plan fp4_plan(int T, int N, int E, int num_kb, int num_sms) {
     }
   }
   return p;
+}
+
+cudaError_t take_fp4_status(int* v) {
+  cudaError_t e = cudaDeviceSynchronize();
+  if (e == cudaSuccess) e = cudaMemcpyFromSymbol(v, product_status, sizeof(int));
+  const int zero = 0;
+  if (e == cudaSuccess && *v != 0) e = cudaMemcpyToSymbol(product_status, &zero, sizeof(int));
+  return e;
 }
 
 cudaError_t launch_gemm_fp4(int format, const CUtensorMap& tw, const CUtensorMap& tx, Fp4GemmArgs a, void* workspace,

@@ -378,6 +378,8 @@ struct Fp4Plan {
 Fp4Plan fp4_plan(int T, int N, int E, int num_kb, int num_sms);
 // Scratch that the plan's kernels need (16-byte aligned), or 0.
 int64_t fp4_workspace(int format, int T, int N, int E, int num_kb, const Fp4Plan& p);
+// Synchronises the device; reads and clears the status bits of its products that were given no word for them.
+cudaError_t take_fp4_status(int* v);
 cudaError_t launch_gemm_fp4(int format, const CUtensorMap& tm_w, const CUtensorMap& tm_x, Fp4GemmArgs a,
                             void* workspace, const Fp4Plan& p, int num_sms, cudaStream_t s);
 

@@ -277,6 +277,15 @@ moe_status moe_fp4_set_wait_timeout(uint64_t timeout_ns) {
   return MOE_OK;
 }
 
+moe_status moe_fp4_get_status(void) {
+  int v = 0;
+  if (take_fp4_status(&v) != cudaSuccess) {
+    cudaGetLastError();
+    return MOE_ERR_CUDA;
+  }
+  return v & kStatusTimeout ? MOE_ERR_TIMEOUT : MOE_OK;
+}
+
 int64_t moe_fp4_linear_workspace_bytes(int32_t format, int32_t T, int32_t N, int32_t K, int32_t E) {
   if (!fp4_format_ok(format) || !product_shape_ok(T, N, K, E) || K % 32 != 0 || T == 0 || T > kMaxQuantized / K)
     return 0;

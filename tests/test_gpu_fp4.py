@@ -460,3 +460,24 @@ def test_waits_that_run_out(fmt, E, T, N, K):
         moe.fp4_set_wait_timeout(2_000_000_000)
     status.zero_()
     assert torch.equal(want, moe.fp4_linear(x, w, ws, fmt, offsets=off, status=status)) and status.item() == 0
+
+
+def test_waits_that_run_out_are_told_without_a_status_word():
+    T, N, K = 1, 2304, 262144
+    w = torch.randint(0, 256, (N, K // 2), device="cuda", dtype=torch.uint8)
+    ws = torch.randint(118, 124, (N, K // 32), device="cuda", dtype=torch.uint8)
+    x = torch.randn((T, K), device="cuda").to(torch.bfloat16)
+    want = moe.fp4_linear(x, w, ws, "mxfp4")
+    assert moe.fp4_status() == moe.MOE_OK
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    try:
+        moe.fp4_set_wait_timeout(1000)
+        moe.fp4_linear(x, w, ws, "mxfp4", status=status)
+        assert status.item() == 1 and moe.fp4_status() == moe.MOE_OK   # the caller's own word
+        moe.fp4_linear(x, w, ws, "mxfp4")
+        moe.fp4_matmul(*moe.quantize_fp4(x, "mxfp4"), w, ws, "mxfp4")
+    finally:
+        moe.fp4_set_wait_timeout(2_000_000_000)
+    assert moe.fp4_status() == moe.MOE_ERR_TIMEOUT
+    assert moe.fp4_status() == moe.MOE_OK      # reading clears it
+    assert torch.equal(want, moe.fp4_linear(x, w, ws, "mxfp4")) and moe.fp4_status() == moe.MOE_OK
