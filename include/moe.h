@@ -529,14 +529,14 @@ MOE_API moe_status moe_dequantize_fp4(int32_t format, const uint8_t* codes, cons
 
 /*
  * y[t, n] = sum_k x[t, k] w[g, n, k] over the values that codes and scales stand for, accumulated
- * in fp32 and rounded once to y's type.
+ * in fp32, multiplied by the tensor scales' product and rounded to y's type.
  *   x [T, K/2], w [E, N, K/2] codes, 16-byte aligned; K % 32 == 0
  *   x_scales, w_scales: K/32 or K/16 bytes per row, rows *_scale_stride bytes apart; nothing
  *          behind a row's last scale is read. Where the call needs no workspace, base and
  *          stride are multiples of 8 (MXFP4) or 16 (NVFP4) bytes (moe_fp4_pad_scales makes such
  *          rows of others); otherwise any
- *   x_tensor_scale fp32 [1], w_tensor_scale fp32 [E] (device) or NULL; NVFP4 only. The product of
- *          the two is taken in fp32, and has to be finite there
+ *   x_tensor_scale fp32 [1], w_tensor_scale fp32 [E] (device) or NULL; NVFP4 only. Their product
+ *          need not be a normal fp32 number where the results are
  *   offsets int32 [E + 1] device: rows offsets[g] .. offsets[g + 1] meet w[g]. Rows in none of
  *          these ranges (behind the last, in front of the first) are left as they were. Values are
  *          clamped to [0, T] and to ascending order. NULL: E = 1, every row.

@@ -374,6 +374,27 @@ __device__ __forceinline__ void store_pairs(const Fp4GemmArgs& a, int row0, int 
       out[static_cast<int64_t>(j) * a.N + n] = static_cast<uint16_t>(p[j / 2] >> (16 * (j & 1)));
 }
 
+// The two tensor scales as (first, then) factors of an accumulator. Their product alone (first = 1) where it is a
+// normal number. Two scales far apart from 1 may multiply to none although the results are: accumulators are 0 or
+// between 2^-20 (half times half, with the least scales) and 2^41, so 2^-+80 times the product's mantissa keeps them
+// normal numbers, and the rest is a power of two, cut off where every result is 0 or infinite.
+__device__ __noinline__ float2 far_scales(float xts, float wts) {
+  if (!(fabsf(xts) < INFINITY && fabsf(wts) < INFINITY)) return make_float2(1.0f, xts * wts);
+  int ex, ew;
+  const float f = frexpf(xts, &ex) * frexpf(wts, &ew);
+  const int e = ex + ew;
+  return e < 0 ? make_float2(f * 0x1p-80f, ldexpf(1.0f, max(e + 80, -126)))
+               : make_float2(f * 0x1p80f, ldexpf(1.0f, min(e - 80, 127)));
+}
+__device__ __forceinline__ float2 tensor_scales(float xts, float wts) {
+  const float m = xts * wts;
+  return fabsf(m) >= 0x1p-126f && fabsf(m) < INFINITY ? make_float2(1.0f, m) : far_scales(xts, wts);
+}
+__device__ __forceinline__ void scale_16(uint32_t (&r)[16], float first) {
+#pragma unroll
+  for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(first * __uint_as_float(r[j]));
+}
+
 // 16 accumulator columns (tokens) scaled and rounded to 16 bits, as pairs.
 __device__ __forceinline__ void pack_16(bool bf, float alpha, const uint32_t (&r)[16], uint32_t (&v)[8]) {
 #pragma unroll
@@ -389,6 +410,25 @@ __device__ __forceinline__ void store_f32(const Fp4GemmArgs& a, const Tile& tl, 
   for (int j = 0; j < 16; ++j) {
     if (c0 + j < tl.rows) *p = alpha * __uint_as_float(r[j]);
     p += a.N;
+  }
+}
+
+// The same in either width for scales with a factor that comes first, from TMEM. Out of line and with plain arguments:
+// a test of that factor in the 16-bit path costs it 1 %, a reference to the kernel's arguments 4 %.
+__device__ __noinline__ void store_far(void* out, int out_dtype, int N, uint32_t taddr, int row0, int n, int nrows,
+                                       float first, float alpha) {
+  uint32_t r[16];
+  tmem_ld16(taddr, r);
+  tmem_ld_wait();
+  if (n >= N) return;
+  scale_16(r, first);
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    if (j >= nrows) break;
+    const float v = alpha * __uint_as_float(r[j]);
+    const int64_t at = static_cast<int64_t>(row0 + j) * N + n;
+    if (out_dtype == kValFp32) static_cast<float*>(out)[at] = v;
+    else static_cast<uint16_t*>(out)[at] = static_cast<uint16_t>(pack_pair(out_dtype == kValBf16, v, 0.0f));
   }
 }
 
@@ -747,10 +787,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       tc_fence_after();
       if constexpr (!kSplit) {
-        const float alpha = args.w_ts ? xts * __ldg(args.w_ts + tl.g) : xts;
+        const float2 scales = args.w_ts ? tensor_scales(xts, __ldg(args.w_ts + tl.g)) : make_float2(1.0f, xts);
+        const float alpha = scales.y;
         const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * C::kAccCols;
         const int mine = q * 32 + lane;  // this lane's row of the tile's first half
-        if (args.out_dtype == kValFp32) {
+        if (scales.x != 1.0f) {
+          for (int c0 = cfirst; c0 < tl.rows; c0 += 16 * C::kEpiGroups)
+            for (int h = 0; h < kHalves; ++h)
+              store_far(args.out, args.out_dtype, args.N, tb + h * kBN + c0, tl.row0 + c0, tl.col0 + mine + h * 128,
+                        tl.rows - c0, scales.x, scales.y);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&tempty[acc]);
+        } else if (args.out_dtype == kValFp32) {
 #pragma unroll 1
           for (int c0 = cfirst; c0 < tl.rows; c0 += 16 * C::kEpiGroups) {
 #pragma unroll
@@ -835,7 +884,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = 0; j < 16; ++j)
           r[j] = __float_as_uint(__uint_as_float(r[j]) + part[(p * kBN + j) * 128]);
       const float xts = args.x_ts ? __ldg(args.x_ts) : 1.0f;
-      const float alpha = args.w_ts ? xts * __ldg(args.w_ts + tl.g) : xts;
+      const float2 scales = args.w_ts ? tensor_scales(xts, __ldg(args.w_ts + tl.g)) : make_float2(1.0f, xts);
+      const float alpha = scales.y;
+      if (scales.x != 1.0f) scale_16(r, scales.x);
       const int m = q * 32 + lane;
       const bool vec_out = args.N % 4 == 0 && (reinterpret_cast<uintptr_t>(args.out) & 7) == 0;
       if (args.out_dtype == kValFp32) {

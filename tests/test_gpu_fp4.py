@@ -481,3 +481,29 @@ def test_waits_that_run_out_are_told_without_a_status_word():
     assert moe.fp4_status() == moe.MOE_ERR_TIMEOUT
     assert moe.fp4_status() == moe.MOE_OK      # reading clears it
     assert torch.equal(want, moe.fp4_linear(x, w, ws, "mxfp4")) and moe.fp4_status() == moe.MOE_OK
+
+
+@pytest.mark.parametrize("x_ts,w_ts,unit", [
+    (1e-22, 1e-20, 2000.0), (3e-38, 1e-3, 2000.0), (1e-30, 1e-13, 2000.0), (2.0 ** -149, 1.0, 2000.0), (1e-3, 1e-41, 2000.0),
+    (1e20, 1e20, 2.0 ** -8), (3e38, 2.0, 2.0 ** -8), (3e38, 1e-38, 1.0), (1e-40, 2e38, 1.0)])
+@pytest.mark.parametrize("T,K", [(5, 1024), (40, 96), (230, 544)])
+def test_matmul_far_tensor_scales(x_ts, w_ts, unit, T, K):
+    """Two tensor scales whose product is no ordinary 32-bit number, where the results are ordinary ones."""
+    N = 130
+    x = torch.randn((T, K), generator=_gen(T)) * unit
+    w = torch.randn((N, K), generator=_gen(K)) * unit
+    xc, xs, _ = ref.quantize(x.double().numpy(), "nvfp4")
+    wc, wsc, _ = ref.quantize(w.double().numpy(), "nvfp4")
+    x_ts, w_ts = (torch.tensor([v], dtype=torch.float32) for v in (x_ts, w_ts))
+    dev = [torch.from_numpy(a).cuda() for a in (xc, xs, wc, wsc)]
+    xv = ref.values(xc, xs, "nvfp4", x_ts.double().numpy())
+    wv = ref.values(wc, wsc, "nvfp4", w_ts.double().numpy())
+    want = xv @ wv.T
+    for out in (torch.float32, torch.bfloat16):
+        y = moe.fp4_matmul(*dev, "nvfp4", x_tensor_scale=x_ts.cuda(), w_tensor_scale=w_ts.cuda(), out_dtype=out)
+        # below the normal range results have a fixed step: 2^-149 in 32 bits, 2^-133 in bfloat16
+        step = 2.0 ** -149 + (2.0 ** -133 if out == torch.bfloat16 else 0.0)
+        err = np.abs(y.double().cpu().numpy() - want)
+        b = _bound(xv, wv, want, out) + step
+        assert (err <= b).all(), (err / b).max()
+        assert np.abs(want).max() > 100 * step      # the bound says something
