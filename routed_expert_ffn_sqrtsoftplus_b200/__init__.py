@@ -456,6 +456,11 @@ def _fp4_workspace_bytes(linear, device, *shape):
     return (L.moe_fp4_linear_workspace_bytes if linear else L.moe_fp4_workspace_bytes)(*shape)
 
 
+def _workspace_size(linear, *shape):
+    # kept by the device that the library plans for: the current one, which need not be the tensors' (a call that is refused)
+    return _fp4_workspace_bytes(linear, torch._C._cuda_getDevice(), *shape)
+
+
 def fp4_set_wait_timeout(ns: int):
     """Limit of the device-side waits of the FP4 products from now on (the process's; default 2 s)."""
     if not 1 <= ns < 1 << 64:
@@ -503,7 +508,7 @@ def fp4_matmul(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_scale
     if status is not None:
         _arg(status, "status", torch.int32, (1,), x)
     xss, wss = x_scales.shape[1], w_scales.shape[-1]
-    nbytes = _fp4_workspace_bytes(False, x.device.index, f, T, N, K, E)
+    nbytes = _workspace_size(False, f, T, N, K, E)
     if nbytes == 0:       # the scales are read as they are: aligned rows
         w_scales, wss = _aligned_scales(w_scales, f)
         x_scales, xss = _aligned_scales(x_scales, f)
@@ -540,9 +545,9 @@ def fp4_linear(x: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor, fmt: st
     wss = w_scales.shape[-1]
     # scales that are read as they are; rows that no base aligns the call itself copies
     if w_scales.data_ptr() % 16 != 0 and wss % (16 if f else 8) == 0 and (
-            _fp4_workspace_bytes(False, x.device.index, f, T, N, K, E) == 0):
+            _workspace_size(False, f, T, N, K, E) == 0):
         w_scales, wss = _aligned_scales(w_scales, f)
-    nbytes = _fp4_workspace_bytes(True, x.device.index, f, T, N, K, E)
+    nbytes = _workspace_size(True, f, T, N, K, E)
     space = _bytes(x, nbytes)
     p = _Fp4Product(f, T, N, K, E, _VALUE_DTYPES[out.dtype], x.data_ptr(), None, 0, x_ts, w.data_ptr(),
                     w_scales.data_ptr(), wss, w_ts, _addr(offsets), out.data_ptr(), space.data_ptr(), nbytes,

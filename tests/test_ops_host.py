@@ -201,3 +201,25 @@ def test_wait_limit_refusals(L):
     for ns in (0, -1, 1 << 64):
         with pytest.raises(ValueError):
             moe.fp4_set_wait_timeout(ns)
+
+
+def test_workspace_sizes_are_kept_by_the_device_that_they_were_planned_for(monkeypatch):
+    """A call under another current device is refused, but may not leave that device's size behind for the tensors' own."""
+    current = [0]
+
+    class Library:
+        def moe_fp4_workspace_bytes(self, *shape):
+            return 100 + current[0]
+
+        moe_fp4_linear_workspace_bytes = moe_fp4_workspace_bytes
+
+    monkeypatch.setattr(moe, "lib", Library)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: current[0], raising=False)
+
+    moe._fp4_workspace_bytes.cache_clear()
+    try:
+        for dev in (0, 1, 0):
+            current[0] = dev
+            assert moe._workspace_size(False, 0, 96, 64, 64, 1) == moe._workspace_size(True, 0, 96, 64, 64, 1) == 100 + dev
+    finally:
+        moe._fp4_workspace_bytes.cache_clear()
