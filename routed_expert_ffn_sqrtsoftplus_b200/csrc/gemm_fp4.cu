@@ -1098,7 +1098,7 @@ static int max_clusters(int size) {
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes) != cudaSuccess ||
       cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
     cudaGetLastError();
-    n = 0;
+    return 0;  // not kept: the next call asks again
   }
   known[dev][size].store(n + 1, std::memory_order_relaxed);
   return n;
