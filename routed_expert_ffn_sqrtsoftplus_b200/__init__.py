@@ -305,12 +305,20 @@ def route(logits: torch.Tensor, top_k: int, *, score: str = "softmax", bias: Opt
     descending order, lower expert first on a tie; the weights are the scores without the bias, divided by their
     sum with ``renormalize``, times route_scale. A logit of -inf takes its expert out; a slot without an expert
     has index -1 and weight 0. A row that is not finite (NaN or +inf) gets experts 0..k-1 with NaN weights.
+
+    Where autograd records and the logits require grad, the weights carry their graph (route_backward; the bias only
+    selects and gets no gradient); topk_idx and topk_w may not be given then, as with torch's out arguments. As with
+    torch's own operators, a step that is captured with its backward pass needs leaves of which no eager graph lives on.
     """
     if stream is not None:
         with _on_stream(stream):
             return route(logits, top_k, score=score, bias=bias, n_groups=n_groups, topk_groups=topk_groups,
                          group_score=group_score, renormalize=renormalize, route_scale=route_scale,
                          topk_idx=topk_idx, topk_w=topk_w)
+    if logits.requires_grad and torch.is_grad_enabled():
+        if topk_idx is not None or topk_w is not None:
+            raise ValueError("topk_idx and topk_w may not be given where the logits require grad")
+        return _Route.apply(logits, top_k, score, bias, n_groups, topk_groups, group_score, renormalize, route_scale)
     T, E, rs, code = _rows(logits, "logits")
     if bias is not None:
         _arg(bias, "bias", torch.float32, (E,), logits)
@@ -348,6 +356,30 @@ def route_backward(grad_w: torch.Tensor, logits: torch.Tensor, topk_idx: torch.T
     _check(lib().moe_route_backward(cfg, grad_w.data_ptr(), logits.data_ptr(), code, rs, topk_idx.data_ptr(), T,
                                     out.data_ptr(), _current(logits)), "moe_route_backward")
     return out
+
+
+class _Route(torch.autograd.Function):
+    """route() in a graph: the selection is held fixed, the weights' gradient becomes the logits'."""
+
+    @staticmethod
+    def forward(ctx, logits, top_k, score, bias, n_groups, topk_groups, group_score, renormalize, route_scale):
+        idx, w = route(logits, top_k, score=score, bias=bias, n_groups=n_groups, topk_groups=topk_groups,
+                       group_score=group_score, renormalize=renormalize, route_scale=route_scale)
+        ctx.mark_non_differentiable(idx)
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(logits, idx)
+        ctx.how = score, renormalize, route_scale
+        return idx, w
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, _, grad_w):
+        if grad_w is None:
+            return (None,) * 9
+        logits, idx = ctx.saved_tensors
+        score, renormalize, route_scale = ctx.how
+        return (route_backward(grad_w.contiguous(), logits, idx, score=score, renormalize=renormalize,
+                               route_scale=route_scale),) + (None,) * 8
 
 
 def _fp4_format(fmt: str) -> int:
@@ -526,7 +558,8 @@ def fp4_linear(x: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor, fmt: st
                status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """y = x w^T with x [T, K] (bfloat16, float16 or float32) quantised to fmt first, then fp4_matmul.
 
-    w, w_scales, the tensor scales, offsets, out and status as there; y has x's dtype unless out says otherwise.
+    w, w_scales, the tensor scales, offsets, out and status as there; y has x's dtype unless out says otherwise, and
+    no graph.
     """
     if stream is not None:
         with _on_stream(stream):
@@ -681,7 +714,7 @@ class MoELayer:
     def forward_routed(self, x: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tensor,
                        out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
         """The layer with a given routing (route()'s, or any other): experts topk_idx int32 [T, top_k], -1 for an
-        empty slot, with weights topk_w fp32 [T, top_k] as they are."""
+        empty slot, with weights topk_w fp32 [T, top_k] as they are. As in every call of the layer y has no graph."""
         if stream is not None:
             with _on_stream(stream):
                 return self.forward_routed(x, topk_idx, topk_w, out)

@@ -413,3 +413,50 @@ def test_route_low_logits_without_renormalisation(kind, dtype):
     want = _grad_ref(far.double().cpu().numpy(), idx.cpu().numpy(), g.double().cpu().numpy(), kind, False, 1.5)
     # one term an element: the bound is relative to itself
     assert (np.abs(got - want) <= (64 * 2.0 ** -24 + torch.finfo(DT[dtype]).eps / 2) * np.abs(want)).all()
+
+
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid", "sqrtsoftplus"])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_route_weights_carry_the_graph_of_their_logits(kind, renorm, dtype):
+    z = _logits(19, 70, dtype, 21, off=2, pad=2).detach().clone().requires_grad_(True)
+    bias = torch.linspace(-0.1, 0.1, 70).cuda().requires_grad_(True)
+    kw = dict(score=kind, renormalize=renorm, route_scale=2.5)
+    idx, w = moe.route(z, 6, bias=bias, n_groups=7, topk_groups=4, **kw)
+    i0, w0 = moe.route(z.detach(), 6, bias=bias.detach(), n_groups=7, topk_groups=4, **kw)
+    assert torch.equal(idx, i0) and torch.equal(w.detach(), w0) and not idx.requires_grad
+    up = torch.randn((19, 6), generator=torch.Generator().manual_seed(5)).cuda()
+    (w * up).sum().backward()
+    assert torch.equal(z.grad, moe.route_backward(up, z.detach(), idx, **kw)) and bias.grad is None
+    # an expanded gradient, and none at all
+    z.grad = None
+    idx, w = moe.route(z, 6, **kw)
+    w.sum().backward()
+    assert torch.equal(z.grad, moe.route_backward(torch.ones_like(up), z.detach(), idx, **kw))
+    with torch.no_grad():
+        assert not moe.route(z, 6, **kw)[1].requires_grad
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    idx, w = moe.route(z, 6, stream=s, **kw)
+    torch.cuda.current_stream().wait_stream(s)
+    assert torch.equal(torch.autograd.grad(w.sum(), z)[0], z.grad)
+    with pytest.raises(ValueError):
+        moe.route(z, 6, topk_w=torch.empty((19, 6), device="cuda"), **kw)
+    with pytest.raises(RuntimeError):   # its gradient has none of its own
+        torch.autograd.grad(torch.autograd.grad(moe.route(z, 6, **kw)[1].sum(), z, create_graph=True)[0].sum(), z)
+
+
+def test_route_and_its_gradient_in_a_captured_step():
+    z = _logits(40, 64, "fp32", 22).detach().clone().requires_grad_(True)
+    up = torch.randn((40, 4), generator=torch.Generator().manual_seed(6)).cuda()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        idx, w = moe.route(z, 4, score="sigmoid")
+        d = torch.autograd.grad(w, z, up)[0]
+    with torch.no_grad():
+        z.copy_(_logits(40, 64, "fp32", 23))
+    graph.replay()
+    torch.cuda.synchronize()
+    i0, w0 = moe.route(z.detach(), 4, score="sigmoid")
+    assert torch.equal(idx, i0) and torch.equal(w.detach(), w0)
+    assert torch.equal(d, moe.route_backward(up, z.detach(), i0, score="sigmoid"))
