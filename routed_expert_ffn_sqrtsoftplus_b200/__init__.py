@@ -234,16 +234,20 @@ def _current(t: torch.Tensor) -> int:
 
 
 # A call's time on few rows is the host's: an output through new_empty takes 1.9 us of it, through the
-# allocator's own entry 0.8 (on the current device, where the library wants every tensor to be).
+# allocator's own entry 0.8 (on the current device, where the library wants every tensor to be). That entry passes by
+# the dispatcher: not under a dispatch mode, for tensors of other classes, or where fresh memory is to be filled.
 try:
+    from torch._C import _cuda_getDevice, _get_deterministic_algorithms, _len_torch_dispatch_stack
     from torch._C._dynamo.guards import _empty_strided_cuda
 except ImportError:
     _empty_strided_cuda = None
+_PLAIN = (torch.Tensor, torch.nn.Parameter)
 
 
 def _empty(ref: torch.Tensor, rows: int, cols: int, dtype) -> torch.Tensor:
     """A matrix for a call's results, on ref's device."""
-    if _empty_strided_cuda is None or ref.get_device() != torch._C._cuda_getDevice():
+    if (_empty_strided_cuda is None or type(ref) not in _PLAIN or ref.get_device() != _cuda_getDevice() or
+            _len_torch_dispatch_stack() or _get_deterministic_algorithms()):
         return ref.new_empty((rows, cols), dtype=dtype)
     return _empty_strided_cuda((rows, cols), (cols, 1), dtype)
 
@@ -488,9 +492,9 @@ def _fp4_workspace_bytes(linear, device, *shape):
     return (L.moe_fp4_linear_workspace_bytes if linear else L.moe_fp4_workspace_bytes)(*shape)
 
 
-def _workspace_size(linear, *shape):
+def _workspace_size(linear, f, T, N, K, E):
     # kept by the device that the library plans for: the current one, which need not be the tensors' (a call that is refused)
-    return _fp4_workspace_bytes(linear, torch._C._cuda_getDevice(), *shape)
+    return _fp4_workspace_bytes(linear, torch._C._cuda_getDevice(), f, T, N, K, E)
 
 
 def fp4_set_wait_timeout(ns: int):

@@ -460,3 +460,35 @@ def test_route_and_its_gradient_in_a_captured_step():
     i0, w0 = moe.route(z.detach(), 4, score="sigmoid")
     assert torch.equal(idx, i0) and torch.equal(w.detach(), w0)
     assert torch.equal(d, moe.route_backward(up, z.detach(), i0, score="sigmoid"))
+
+
+def test_outputs_come_through_the_dispatcher_where_something_listens():
+    """A dispatch mode sees the outputs' allocation, and under fake tensors they are fake."""
+    from torch.utils._python_dispatch import TorchDispatchMode
+    from torch._subclasses.fake_tensor import FakeTensor, FakeTensorMode
+
+    class Seen(TorchDispatchMode):
+        def __init__(self):
+            super().__init__()
+            self.made = []
+
+        def __torch_dispatch__(self, func, types, args=(), kwargs=None):
+            out = func(*args, **(kwargs or {}))
+            if "empty" in str(func):
+                self.made.append(out.data_ptr())
+            return out
+
+    z = _logits(5, 20, "fp32", 1)
+    want = moe.route(z, 3)
+    with Seen() as seen:
+        idx, w = moe.route(z, 3)
+    assert {idx.data_ptr(), w.data_ptr()} <= set(seen.made)
+    assert torch.equal(idx, want[0]) and torch.equal(w, want[1])
+    with FakeTensorMode():
+        fake = torch.empty((5, 20), device="cuda")
+        assert isinstance(moe._empty(fake, 5, 3, torch.int32), FakeTensor)
+    torch.use_deterministic_algorithms(True)
+    try:   # memory that nothing writes is filled there
+        assert bool(torch.isnan(moe._empty(z, 4, 64, torch.float32)).all())
+    finally:
+        torch.use_deterministic_algorithms(False)
