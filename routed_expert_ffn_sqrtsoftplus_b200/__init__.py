@@ -292,7 +292,7 @@ def _route_config(E, k, n_groups, topk_groups, score, group_score, renormalize, 
         raise ValueError(f"score must be one of {tuple(SCORES)}")
     if group_score not in ("top2", "max"):
         raise ValueError("group_score must be 'top2' or 'max'")
-    if not 1 <= k <= E or max(n_groups, topk_groups) >= 1 << 31:
+    if not 1 <= k <= E or max(abs(n_groups), abs(topk_groups)) >= 1 << 31:
         raise ValueError(f"top_k must be 1 .. {E}, got {k}, with fewer than 2^31 groups")
     return _RouteConfig(E, k, n_groups, topk_groups, SCORES[score], group_score == "top2", bool(renormalize),
                         route_scale)

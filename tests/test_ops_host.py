@@ -223,3 +223,12 @@ def test_workspace_sizes_are_kept_by_the_device_that_they_were_planned_for(monke
             assert moe._workspace_size(False, 0, 96, 64, 64, 1) == moe._workspace_size(True, 0, 96, 64, 64, 1) == 100 + dev
     finally:
         moe._fp4_workspace_bytes.cache_clear()
+
+
+def test_group_counts_far_below_zero_are_refused(L):
+    # cut to 32 bits they would be 1
+    for args in ((1 - (1 << 32), 1), (1, 1 - (1 << 32)), (2 - (1 << 33), 1)):
+        with pytest.raises(ValueError):
+            moe._route_config(8, 2, *args, "softmax", "max", True, 1.0)
+    # and those that fit go to the library, which refuses them
+    assert L.moe_route(moe._route_config(8, 2, -1, 1, "softmax", "max", True, 1.0), FAKE, 2, 8, None, 3, FAKE, FAKE, None) == INV
