@@ -513,7 +513,7 @@ typedef enum {
  *   MXFP4: the rule of moe_quantize_mxfp4.
  *   NVFP4: sf = the E4M3 nearest to amax / (6 ts), at most 448; an element stands for e2m1 * d with
  *          d = sf * ts rounded to fp32, and is the nearest such value (ties to even, at most 6 d);
- *          ts = *tensor_scale (fp32, device, positive), or 1 when NULL. MXFP4 takes NULL. Where d
+ *          ts = *tensor_scale (fp32, device, positive; 0 for a tensor of zeros), or 1 when NULL. MXFP4 takes NULL. Where d
  *          is below fp32's normal range the block's codes are 0.
  * A block holding NaN or infinity gets the scale format's NaN (0xFF, 0x7F) and zero codes.
  * rows * cols <= 2^33 (else MOE_ERR_UNSUPPORTED), for moe_dequantize_fp4 too.

@@ -115,7 +115,8 @@ __device__ __forceinline__ float e4m3_value(uint32_t code) {
   return __half2float(__half(__nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(code), __NV_E4M3)));
 }
 
-// The E4M3 code nearest to amax / (6 ts), ties to even, at most 126 (448).
+// The E4M3 code nearest to amax / (6 ts), ties to even, at most 126 (448); 0 where amax is, also with the ts of 0 that a
+// tensor of zeros calibrates to.
 __device__ __forceinline__ uint32_t e4m3_scale(float amax, float ts) {
   // far out, both by one power of two, so that neither the reciprocal nor a difference leaves the normal range
   // (where amax does, the code is 0 or 126 with or without it)
@@ -136,7 +137,7 @@ __device__ __forceinline__ uint32_t e4m3_scale(float amax, float ts) {
     const float s = fmaf(-3.0f * (e4m3_value(c) + e4m3_value(up)), ts, amax);
     if (s > 0.f || (s == 0.f && (c & 1u))) c = up;
   }
-  return c;
+  return amax == 0.f ? 0u : c;
 }
 
 // Eight scaled values to a word of E2M1 codes, the first in the lowest nibble: nearest, ties to even, at most 6.

@@ -507,3 +507,18 @@ def test_matmul_far_tensor_scales(x_ts, w_ts, unit, T, K):
         b = _bound(xv, wv, want, out) + step
         assert (err <= b).all(), (err / b).max()
         assert np.abs(want).max() > 100 * step      # the bound says something
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+def test_tensor_of_zeros_with_the_scale_that_it_calibrates_to(dtype):
+    x = torch.zeros((40, 96), dtype=DT[dtype], device="cuda")
+    x[1] = -0.0
+    ts = (x.abs().max().float() / 2688.0).reshape(1)
+    assert ts.item() == 0.0
+    codes, scales = moe.quantize_fp4(x, "nvfp4", ts)
+    assert not bool(scales.any()) and not bool((codes & 0x77).any())
+    assert not bool(moe.dequantize_fp4(codes, scales, "nvfp4", ts, dtype=torch.float32).any())
+    w, ws, wts = _weights(1, 64, 96, "nvfp4", 3)
+    for T in (3, 40):
+        y = moe.fp4_linear(x[:T], w[0], ws[0], "nvfp4", x_tensor_scale=ts, w_tensor_scale=wts)
+        assert bool((y == 0).all())
