@@ -522,3 +522,22 @@ def test_tensor_of_zeros_with_the_scale_that_it_calibrates_to(dtype):
     for T in (3, 40):
         y = moe.fp4_linear(x[:T], w[0], ws[0], "nvfp4", x_tensor_scale=ts, w_tensor_scale=wts)
         assert bool((y == 0).all())
+
+
+@pytest.mark.parametrize("fmt", FMT)
+@pytest.mark.parametrize("T", [64, 700])
+def test_experts_of_unlike_loads(fmt, T):
+    """Most rows, or all of them, on one expert of many: tile shapes go by the mean load."""
+    E, N, K = 32, 264, 288
+    x = _x(T, K, "bf16", T)
+    w, ws, wts = _weights(E, N, K, fmt, 9)
+    _, _, xv = ref.quantize(x.double().numpy(), fmt)
+    for sizes in ([0] * 7 + [T] + [0] * 24, [1] * 31 + [T - 31], [T - 31] + [1] * 31):
+        off = torch.tensor([0] + list(np.cumsum(sizes)), dtype=torch.int32)
+        y = moe.fp4_linear(x.cuda(), w, ws, fmt, w_tensor_scale=wts, offsets=off.cuda()).double().cpu().numpy()
+        for g in range(E):
+            a, b = int(off[g]), int(off[g + 1])
+            if a < b:
+                wv = ref.values(w[g].cpu().numpy(), ws[g].cpu().numpy(), fmt, None if wts is None else wts.cpu().numpy()[g])
+                want = xv[a:b] @ wv.T
+                assert (np.abs(y[a:b] - want) <= _bound(xv[a:b], wv, want, torch.bfloat16)).all(), g

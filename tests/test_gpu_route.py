@@ -492,3 +492,58 @@ def test_outputs_come_through_the_dispatcher_where_something_listens():
         assert bool(torch.isnan(moe._empty(z, 4, 64, torch.float32)).all())
     finally:
         torch.use_deterministic_algorithms(False)
+
+
+# ------------------------------------------------------------------ given routings of every kind of layer
+@pytest.fixture(scope="module", params=["bf16", "mxfp4", "mxfp8"])
+def any_layer(request, cuda_device):
+    """(layer, its experts' float64 matrices, whether rows meet them in MXFP8)."""
+    from oracle import mx as omx
+    lay = synth.make_layer(WL.with_tokens(400), device="cpu")
+    q, fmt = None, request.param
+    if fmt != "bf16":
+        quant = omx.quantize_mxfp4_packed if fmt == "mxfp4" else omx.quantize_mxfp8
+        q = {}
+        for n, s in (("w1", "s1"), ("w3", "s3"), ("w2", "s2")):
+            q[n], q[s] = (torch.from_numpy(np.ascontiguousarray(v)) for v in quant(parity.f64(lay[n])))
+    dev = {k: (v.to(cuda_device) if isinstance(v, torch.Tensor) else v) for k, v in lay.items()}
+    layer = moe.MoELayer.from_layer(dev, top_k=WL.k, max_tokens=400,
+                                    **({} if q is None else {"mx": {n: v.to(cuda_device) for n, v in q.items()}}))
+    yield dev["x"], layer, parity.LayerExperts(lay, q)
+    layer.close()
+
+
+def _routed_ref(x, ex, idx, w):
+    from oracle import moe as om
+    y = np.zeros(x.shape)
+    for j in range(ex.n_shared):
+        y += om.expert_forward(x, *ex.shared(j), WL.swiglu_limit)[0]
+    for e in range(ex.n_routed):
+        t, r = np.nonzero(idx == e)
+        if len(t):
+            o, _ = om.expert_forward(x[t], *ex.routed(e), WL.swiglu_limit, mx_act=ex.routed_is_mx)
+            np.add.at(y, t, o * w[t, r][:, None])
+    return y
+
+
+@pytest.mark.parametrize("T", [1, 7, 32, 33, 70, 400])
+@pytest.mark.parametrize("how", ["holes", "twice", "one expert", "empty"])
+def test_forward_routed_of_every_layer(any_layer, T, how):
+    """Empty slots, rows without any expert, experts named twice by a token, every slot the same expert, no expert."""
+    xs, layer, ex = any_layer
+    x = xs[:T].contiguous()
+    g = torch.Generator().manual_seed(T)
+    idx = torch.argsort(torch.rand((T, WL.E), generator=g), 1)[:, :WL.k].int()
+    w = torch.rand((T, WL.k), generator=g) + 0.1
+    if how == "holes":
+        idx[torch.rand(idx.shape, generator=g) < 0.4] = -1
+        idx[T // 2] = -1
+    elif how == "twice":
+        idx[::2, 1] = idx[::2, 0]
+        idx[T // 3] = 5
+    else:
+        idx[:] = 3 if how == "one expert" else -1
+    y = layer.forward_routed(x, idx.cuda(), w.cuda())
+    assert layer.status() == moe.MOE_OK
+    want = _routed_ref(parity.f64(x.cpu()), ex, idx.numpy(), w.double().numpy())
+    assert parity.output_score(y.double().cpu().numpy(), want) < parity.TOL_Y
