@@ -480,8 +480,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tmA);
     tma_prefetch_desc(&tmB);
   }
-  // everything above overlaps the kernel in front (the quantiser, or the scales' arrangement); TMEM is taken
-  // behind it, so that no block waits for a kernel that waits for this block's columns
+  // everything above overlaps a quantiser of few blocks in front (the scales' arrangement lets no kernel start early);
+  // TMEM is taken behind it, so that no block waits for a kernel that waits for this block's columns
   wait_for_previous_kernel();
   if (warp == 1) {
     tmem_alloc(tmem_base_smem, 512);

@@ -22,9 +22,11 @@
 // with more than 32 of either is selected from 64-bit keys as a whole (select_row_f64). So the
 // result is always that of the 64-bit keys.
 //
-// Bound by instructions: 1090 a row of 256 FP32 logits with bias and groups (13.0 us for 8192 rows, of which HBM
-// needs 1.3; 2.5 of 4 issue slots are taken while the SMs are busy, and a row in itself takes 3 us of latencies), 560
-// a row of 128 BF16 logits without either (4.2 us for 4099 rows; HBM 0.2).
+// Bound by instructions: 1080 a row of 256 FP32 logits with bias and groups (13.6 us for 8192 rows, of which HBM
+// needs 1.3; 2.5 of 4 issue slots are taken while the SMs are busy, and a row in itself takes 3 us of latencies), 530
+// a row of 128 BF16 logits without either (4.0 us for 4099 rows; HBM 0.2). A row takes a whole warp whatever E is: 16384 x
+// 64 FP32 11.8 us (HBM 0.8); groups that lanes do not align with go through shared memory: 16384 x 200 BF16 in 8 groups
+// 28.5 us (HBM 1.2).
 #include <cuda_fp16.h>
 
 #include "common.cuh"
@@ -647,7 +649,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32, EPL < 16 ? 1 : sizeof(T) == 
 // One warp per row; lane r holds slot r (an expert named twice adds up). The row is written 16 bytes a
 // lane without the slots' own terms (zeros, or in the dense form -s_e scale sum_j g_j s_j from a row held
 // in registers), and the slots' elements go over it: one warp, so in this order. Bound by HBM's writes: 16384 x
-// 512 FP32, 16 slots, 9.6 us (HBM 5.6), dense 13.5 (10.6; 39 with the row read and exponentiated twice).
+// 512 FP32, 16 slots, 8.9 us (HBM 5.6), dense 13.5 (10.6; 39 with the row read and exponentiated twice).
 template <typename T, bool kDense>
 __global__ void __launch_bounds__(kRouteWarps * 32)
     route_grad_kernel(const float* __restrict__ grad_w, const T* __restrict__ logits, int64_t row_stride,
